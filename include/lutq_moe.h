@@ -1,0 +1,97 @@
+/*
+ * lutq -- mixture of experts: the router and the experts' 4-bit products.
+ *
+ * The conventions of lutq.h and lutq_mx.h hold: caller-owned memory, caller's
+ * stream, nothing enqueued on an error, no scratch memory of the library.
+ */
+#ifndef LUTQ_MOE_H
+#define LUTQ_MOE_H
+
+#include "lutq_mx.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define LUTQ_MOE_MAX_EXPERTS 1024 /* E                         */
+#define LUTQ_MOE_MAX_TOPK 32      /* k, and k <= E             */
+#define LUTQ_MOE_MAX_GROUPS 64
+/* T * k <= LUTQ_MOE_MAX_PAIRS */
+#define LUTQ_MOE_MAX_PAIRS (1 << 24)
+
+enum { LUTQ_MOE_SOFTMAX = 0, LUTQ_MOE_SIGMOID = 1 };
+
+typedef struct lutq_moe_options {
+  int32_t score;      /* LUTQ_MOE_SOFTMAX or _SIGMOID: the score s of an expert   */
+  int32_t groups;     /* experts in `groups` runs of E / groups; 1 = no groups     */
+  int32_t top_groups; /* groups kept per token, <= groups                          */
+  int32_t group_best; /* a group's rank: the sum of its 1 or 2 largest keys        */
+  int32_t renorm;     /* 1: the chosen scores are divided by their sum             */
+  float scale;        /* the weights are multiplied by this                        */
+  int32_t reserved[2];/* must be zero                                              */
+} lutq_moe_options_t;
+
+/* For each token: the k experts with the largest keys, and their weights.
+ *   key     : the logit itself where there is neither a bias nor a sum of two
+ *             keys (the score rises with the logit), else score + bias.
+ *   choice  : the top_groups groups by rank (of equal ones the lower index),
+ *             then the k largest keys in them (of equal ones the lower index),
+ *             in falling order. An expert whose logit is -infinity or whose
+ *             key is NaN or -infinity is never chosen: a token with fewer than
+ *             k experts left (a padded row of -infinities has none) gets id -1
+ *             and weight 0 in the remaining places.
+ *   weights : the chosen experts' scores without the bias; with renorm divided
+ *             by their sum (sigmoid: sum + 1e-20), times scale. A softmax row
+ *             that holds a NaN or +infinity has NaN weights.
+ *
+ *   logits  : device, [T][E] fp32, fp16 or bf16 (`dtype`), row stride ld >= E
+ *             elements, aligned to its element size.
+ *   bias    : device, fp32 [E], or NULL.
+ *   opts    : host; NULL = softmax, no groups, renorm, scale 1.
+ *   ids     : device, int32 [T][k] out.    weights : device, fp32 [T][k] out.
+ *   plan    : device, int32, lutq_moe_plan_ints(T, E, k) entries, out, or NULL:
+ *             [0, E]           offsets: expert e has the pairs at positions
+ *                              offsets[e] .. offsets[e + 1] - 1
+ *             [E + 1, + T * k] order: the pair t * k + j at each position, by
+ *                              expert and within it by rising pair; -1 past
+ *                              offsets[E]
+ *             the rest         what lutq_moe_mlp reads of it.
+ * fp32 arithmetic. T == 0: nothing to do (plan: the offsets are set to 0).
+ * Errors: LUTQ_EINVAL (also k < 1 or > E, groups not dividing E, fewer than
+ * group_best experts in a group), LUTQ_EALIGN, LUTQ_EUNSUPPORTED, LUTQ_EHIP. */
+int lutq_moe_route(const void* logits, int dtype, long long ld, const float* bias, int T, int E,
+                   int k, const lutq_moe_options_t* opts, int32_t* ids, float* weights,
+                   int32_t* plan, void* stream);
+
+/* int32 entries of a plan; 0 for invalid sizes. */
+size_t lutq_moe_plan_ints(int T, int E, int k);
+
+/* The plan of given ids [T][k] (from another router; values outside [0, E)
+ * count as "no expert"), as lutq_moe_route writes it. */
+int lutq_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, void* stream);
+
+/* y[t] = sum_j weights[t][j] * down_e . (silu(gate_e . x[t]) * (up_e . x[t])),
+ * e = ids[t][j], over the places with an expert (y[t] = 0 where there is none).
+ *   gate_up : host descriptor, experts = E, N = 2F (gate rows, then up rows;
+ *             F a multiple of 32), K = D.   down : E, N = D, K = F.
+ *   x       : device, fp16 or bf16 [T][D], row stride ldx, as lutq_mx_matmul.
+ *   y       : device, [T][D] contiguous in `dtype`, 8-byte aligned.
+ *   workspace : device, lutq_moe_workspace_bytes(T, k, D, F), 16-byte aligned.
+ * Sums are fp32; silu(g) * u is rounded to `dtype` in calls of many pairs and
+ * keeps 16 bits of significand in calls of few; each expert's output stays
+ * fp32 until the weighted sum, which runs in the order of j and is rounded
+ * once. No atomics: results repeat bit for bit.
+ * Errors: LUTQ_EINVAL, LUTQ_EMISMATCH (the descriptors do not fit each other),
+ * LUTQ_EALIGN, LUTQ_ESIZE, LUTQ_EUNSUPPORTED (also more than 2^31 output
+ * tiles), LUTQ_EHIP. */
+size_t lutq_moe_workspace_bytes(int T, int k, int D, int F);
+int lutq_moe_mlp(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* gate_up,
+                 const lutq_mx_packed_t* down, const int32_t* ids, const float* weights,
+                 const int32_t* plan, int T, int k, void* workspace, size_t workspace_bytes,
+                 void* y, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LUTQ_MOE_H */

@@ -1,0 +1,131 @@
+/*
+ * lutq -- microscaled 4-bit floating point (MX4): quantization and product.
+ *
+ * Format (OCP Microscaling, MXFP4): every 32 consecutive values along K share
+ * one power-of-two scale; a value is a 4-bit E2M1 code times its scale.
+ *   code  : bit 3 the sign, bits 0-2 the level {0, 0.5, 1, 1.5, 2, 3, 4, 6}.
+ *   scale : one E8M0 byte b, the value 2^(b - 127); 255 is NaN and makes all
+ *           32 values NaN.
+ *   codes  [rows][K/2] bytes, row-major; the value of the even k is in the
+ *          low nibble.
+ *   scales [rows][K/32] bytes, row-major.
+ *
+ * The conventions of lutq.h hold (ownership, streams, status codes, nothing
+ * enqueued on an error, no C++ exception). No entry point here uses scratch
+ * memory of the library, so all of them may be captured into a HIP graph at
+ * any time and run concurrently on different streams.
+ */
+#ifndef LUTQ_MX_H
+#define LUTQ_MX_H
+
+#include "lutq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of float tensors here: LUTQ_WEIGHT_F32 (0), _F16 (1) and
+ * _BF16 (2) of lutq.h. */
+
+/* Limits: 0 <= rows <= 2^31 - 1, K a multiple of 32 (LUTQ_EGROUP otherwise)
+ * and at most LUTQ_MAX_K, rows * K <= LUTQ_MAX_NK. */
+#define LUTQ_MX_BLOCK 32
+
+/* How a block's scale follows from its largest magnitude `top`:
+ *   LUTQ_MX_FLOOR: 2^(floor(log2 top) - 2), the rule of the format's
+ *                  specification; values above 6 scales saturate.
+ *   LUTQ_MX_CEIL : the smallest power of two that is >= top / 6: nothing
+ *                  saturates.
+ * Either is clamped to [2^-127, 2^127]; an all-zero block takes 2^-127. */
+enum { LUTQ_MX_FLOOR = 0, LUTQ_MX_CEIL = 1 };
+
+/* x [rows][K] (element type `dtype`, row stride ldx elements) to codes and
+ * scales. A value is divided by its scale exactly and rounded to the nearest
+ * level, halfway cases to the even code; the sign survives a rounding to 0. A
+ * block holding an infinity or a NaN gets scale 255 and codes 0.
+ *   x      : device, 16-byte aligned, ldx >= K and ldx * element size a
+ *            multiple of 16.
+ *   codes  : device, 4-byte aligned; scales : device.
+ * Errors: LUTQ_EINVAL, LUTQ_EGROUP, LUTQ_EALIGN, LUTQ_EUNSUPPORTED, LUTQ_EHIP. */
+int lutq_mx_quantize(const void* x, int dtype, int rows, int K, long long ldx, int rule,
+                     uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values the codes stand for, [rows][K] contiguous in `dtype`, rounded
+ * once (fp32 and bf16 hold every value with a scale of at most 2^125 exactly).
+ *   codes : 4-byte aligned; x : 16-byte aligned. Errors as lutq_mx_quantize. */
+int lutq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype, int rows, int K,
+                       void* x, void* stream);
+
+/* ---- packed weights ----------------------------------------------------------
+ * `experts` weight matrices [N][K] laid out once for the products (layout
+ * version 1). Rows are cut into tiles of 16 per expert, K into chunks of 128;
+ * ntile = ceil(N/16), nchunk = ceil(K/128), nquad = ceil(nchunk/4). `data`
+ * holds, one after another:
+ *   codes  : [experts][ntile][nchunk] blocks of 64 slots x 16 bytes; slot
+ *            16*q + r holds the 32 codes of row 16*t + r, k = 128*c + 32*q ..
+ *            + 31, in the order of the row-major codes.
+ *   scales : [experts][ntile][nquad][64 slots][4] bytes: byte c%4 of slot
+ *            (c/4, 16*q + r) is the scale of that row and block relative to
+ *            its row: max(0, b - top + 127), `top` being the largest b of the
+ *            row's blocks that hold a nonzero code.
+ *   rows   : [experts][16*ntile] fp32, 2^(top - 127), or NaN if the row has a
+ *            NaN block.
+ * Rows past N and blocks past K hold zeros. */
+#define LUTQ_MX_MAGIC 0x34584D4Cu /* "LMX4" */
+#define LUTQ_MX_LAYOUT_VERSION 1u
+#define LUTQ_MX_MAX_EXPERTS 1024
+
+typedef struct lutq_mx_packed {
+  uint32_t magic, version;
+  int32_t experts, N, K, reserved;
+  uint64_t nbytes; /* lutq_mx_packed_bytes                              */
+  void* data;      /* device, caller-owned, 16-byte aligned             */
+} lutq_mx_packed_t;
+
+/* Bytes lutq_mx_pack writes; 0 for invalid or empty sizes. */
+size_t lutq_mx_packed_bytes(int experts, int N, int K);
+
+/*   codes  : device, [experts][N][K/2], 16-byte aligned.
+ *   scales : device, [experts][N][K/32].
+ *   dst    : device, >= lutq_mx_packed_bytes, 16-byte aligned, not
+ *            overlapping the inputs.
+ *   out    : host, filled on success.
+ * Errors: LUTQ_EINVAL, LUTQ_EGROUP, LUTQ_EALIGN, LUTQ_ESIZE, LUTQ_EUNSUPPORTED
+ * (experts > LUTQ_MX_MAX_EXPERTS or sizes beyond the limits), LUTQ_EHIP. */
+int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N, int K, void* dst,
+                 size_t dst_bytes, lutq_mx_packed_t* out, void* stream);
+
+/* ---- products ------------------------------------------------------------------
+ * y[m, n] = sum_k x[m, k] * w[n, k], one matrix (experts == 1).
+ *   x      : device, fp16 or bf16 (`dtype`) [M][K], row stride ldx elements,
+ *            16-byte aligned, ldx >= K and a multiple of 8.
+ *   y      : device, [M][N] contiguous in `dtype`, 8-byte aligned.
+ * fp32 accumulation on the matrix cores; y is rounded once, to nearest even.
+ * The weights enter exactly, with their row's largest scale taken out and
+ * multiplied onto the fp32 sum, except that bits are lost of values in a
+ * block whose scale is below its row's largest by more than 2^36 (fp16) or
+ * 2^120 (bf16).
+ * path: LUTQ_MX_PATH_AUTO, or one of the two kernels (any M runs on either).
+ * M == 0 or N == 0: nothing to do. K == 0: y is set to zero.
+ * Errors: LUTQ_EINVAL, LUTQ_EMISMATCH, LUTQ_EALIGN, LUTQ_EUNSUPPORTED (more
+ * than 2^31 output tiles of 64 x 64), LUTQ_EHIP. */
+enum {
+  LUTQ_MX_PATH_AUTO = 0,
+  LUTQ_MX_PATH_STREAM = 1, /* weights streamed past 16-64 rows held by a workgroup */
+  LUTQ_MX_PATH_TILE = 2    /* tiles of 64-256 rows through on-chip memory           */
+};
+int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,
+                   int M, int N, int K, int path, void* stream);
+
+/* The same with 4-bit activations: xcodes [M][K/2] and xscales [M][K/32] as
+ * lutq_mx_quantize writes them, both operands in 4 bits on the scaled matrix
+ * instructions; `dtype` (fp16 or bf16) is y's.
+ *   xcodes : 16-byte aligned. */
+int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
+                      void* y, int dtype, int M, int N, int K, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LUTQ_MX_H */

@@ -41,3 +41,15 @@ from ._lib import (  # noqa: F401
     tune_table,
     unpack,
 )
+from ._mx import (  # noqa: F401
+    moe_mlp,
+    moe_plan,
+    moe_route,
+    mx_dequantize,
+    mx_matmul,
+    mx_pack,
+    mx_quantize,
+    MX_BLOCK,
+    MxPacked,
+    Routing,
+)

@@ -28,6 +28,12 @@ EXPORTS = (
     # include/lutq_peaks.h
     "lutq_peak_empty", "lutq_peak_stream_sink_bytes", "lutq_peak_stream", "lutq_peak_mfma",
     "lutq_peak_lds",
+    # include/lutq_mx.h
+    "lutq_mx_quantize", "lutq_mx_dequantize", "lutq_mx_packed_bytes", "lutq_mx_pack",
+    "lutq_mx_matmul", "lutq_mx_matmul_mx",
+    # include/lutq_moe.h
+    "lutq_moe_route", "lutq_moe_plan_ints", "lutq_moe_plan", "lutq_moe_workspace_bytes",
+    "lutq_moe_mlp",
 )
 
 MAX_TYPES = 4
@@ -148,6 +154,8 @@ def load_library():
     lib.lutq_peak_mfma.restype = i32
     lib.lutq_peak_lds.argtypes = [i32, i32, vp, vp]
     lib.lutq_peak_lds.restype = i32
+    from . import _mx
+    _mx.declare(lib)
     _LIB = lib
     return lib
 

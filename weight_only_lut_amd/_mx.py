@@ -1,0 +1,311 @@
+"""ctypes binding of the microscaled 4-bit (MX4) and expert entry points.
+
+Argument marshalling only: every function forwards to the C entry points of
+``include/lutq_mx.h`` and ``include/lutq_moe.h``; tensors are passed as raw
+device pointers and the stream is PyTorch's current one.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import LutqError, WEIGHT_BF16, WEIGHT_F16, WEIGHT_F32, _check, _lib, _on_device
+
+MX_BLOCK = 32
+MX_FLOOR, MX_CEIL = 0, 1
+_RULES = {"floor": MX_FLOOR, "ceil": MX_CEIL}
+MX_PATH_AUTO, MX_PATH_STREAM, MX_PATH_TILE = 0, 1, 2
+_PATHS = {"auto": MX_PATH_AUTO, "stream": MX_PATH_STREAM, "tile": MX_PATH_TILE}
+_TYPES = {torch.float32: WEIGHT_F32, torch.float16: WEIGHT_F16, torch.bfloat16: WEIGHT_BF16}
+_HALF = {torch.float16: WEIGHT_F16, torch.bfloat16: WEIGHT_BF16}
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+_SCORES = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
+
+
+class MxPackedDesc(ctypes.Structure):
+    _fields_ = [
+        ("magic", ctypes.c_uint32), ("version", ctypes.c_uint32),
+        ("experts", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("nbytes", ctypes.c_uint64), ("data", ctypes.c_void_p),
+    ]
+
+
+class MoeOptions(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 2)]
+
+
+def declare(lib):
+    """Argument and result types of the entry points (called once, on load)."""
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+    for name, res, args in (
+            ("lutq_mx_quantize", i32, [vp, i32, i32, i32, i64, i32, vp, vp, vp]),
+            ("lutq_mx_dequantize", i32, [vp, vp, i32, i32, i32, vp, vp]),
+            ("lutq_mx_packed_bytes", sz, [i32, i32, i32]),
+            ("lutq_mx_pack", i32, [vp, vp, i32, i32, i32, vp, sz, vp, vp]),
+            ("lutq_mx_matmul", i32, [vp, i32, i64, vp, vp, i32, i32, i32, i32, vp]),
+            ("lutq_mx_matmul_mx", i32, [vp, vp, vp, vp, i32, i32, i32, i32, vp]),
+            ("lutq_moe_route", i32, [vp, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp]),
+            ("lutq_moe_plan_ints", sz, [i32, i32, i32]),
+            ("lutq_moe_plan", i32, [vp, i32, i32, i32, vp, vp]),
+            ("lutq_moe_workspace_bytes", sz, [i32, i32, i32, i32]),
+            ("lutq_moe_mlp", i32, [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
+
+
+def _raw_stream(device):
+    """The current stream's handle, as an int."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _rows_of(t, name, types):
+    """Type checks of a 2-D tensor with unit column stride; its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in types)}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    rows, cols = t.shape
+    step, unit = t.stride()
+    if rows and ((cols > 1 and unit != 1) or (rows > 1 and step < cols)):
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return step if rows > 1 else cols
+
+
+def _codes_of(pair, name):
+    """(codes, scales) of a microscaled matrix, checked against each other."""
+    codes, scales = pair
+    _check(codes, f"{name} codes", torch.uint8)
+    _check(scales, f"{name} scales", torch.uint8)
+    if codes.dim() < 2 or codes.shape[-1] % (MX_BLOCK // 2):
+        raise ValueError(f"{name} codes must be [..., K / 2] with K a multiple of {MX_BLOCK}")
+    want = (*codes.shape[:-1], codes.shape[-1] * 2 // MX_BLOCK)
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{name} scales have shape {tuple(scales.shape)}, expected {want}")
+    return codes, scales
+
+
+def mx_quantize(x, rule: str = "floor"):
+    """lutq_mx_quantize: fp32, fp16 or bf16 [rows, K] (rows may be strided) ->
+    (codes uint8 [rows, K/2], scales uint8 [rows, K/32])."""
+    ldx = _rows_of(x, "x", _TYPES)
+    if rule not in _RULES:
+        raise ValueError(f"rule must be one of {sorted(_RULES)}")
+    rows, K = x.shape
+    if K % MX_BLOCK:
+        raise ValueError(f"K = {K} is not a multiple of {MX_BLOCK}")
+    _on_device(("x", x))
+    dev = x.device
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((rows, K // MX_BLOCK), dtype=torch.uint8, device=dev)
+    rc = _lib().lutq_mx_quantize(x.data_ptr(), _TYPES[x.dtype], rows, K, ldx, _RULES[rule],
+                                 codes.data_ptr(), scales.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise LutqError(rc, "lutq_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, dtype=torch.bfloat16):
+    """lutq_mx_dequantize: the values [rows, K] (or [..., K]) the codes stand for."""
+    codes, scales = _codes_of((codes, scales), "mx")
+    if dtype not in _TYPES:
+        raise TypeError(f"dtype must be {' or '.join(str(d) for d in _TYPES)}, got {dtype}")
+    _on_device(("codes", codes), ("scales", scales))
+    dev = codes.device
+    K = codes.shape[-1] * 2
+    rows = codes.numel() * 2 // K if K else 0
+    x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=dev)
+    rc = _lib().lutq_mx_dequantize(codes.data_ptr(), scales.data_ptr(), _TYPES[dtype], rows, K,
+                                   x.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise LutqError(rc, "lutq_mx_dequantize")
+    return x
+
+
+class MxPacked:
+    """Packed MX4 weights of one matrix or of several experts: the device
+    buffer plus its host descriptor."""
+
+    def __init__(self, data, desc: MxPackedDesc):
+        self.data = data          # torch uint8 tensor owning the device bytes
+        self.desc = desc
+        self._ref = ctypes.addressof(desc)
+        # the descriptor's fields do not change once packed
+        self.experts, self.N, self.K = desc.experts, desc.N, desc.K
+
+    nbytes = property(lambda self: self.desc.nbytes)
+
+
+def mx_pack(codes, scales) -> MxPacked:
+    """lutq_mx_pack: codes [N, K/2] and scales [N, K/32], or [experts, N, ...],
+    on the GPU -> MxPacked."""
+    codes, scales = _codes_of((codes, scales), "weight")
+    if codes.dim() > 3:
+        raise ValueError("codes must be [N, K/2] or [experts, N, K/2]")
+    _on_device(("codes", codes), ("scales", scales))
+    E = codes.shape[0] if codes.dim() == 3 else 1
+    N, K = codes.shape[-2], codes.shape[-1] * 2
+    nbytes = _lib().lutq_mx_packed_bytes(E, N, K)
+    dst = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=codes.device)
+    desc = MxPackedDesc()
+    rc = _lib().lutq_mx_pack(codes.data_ptr(), scales.data_ptr(), E, N, K, dst.data_ptr(), dst.numel(),
+                             ctypes.addressof(desc), _raw_stream(codes.device))
+    if rc:
+        raise LutqError(rc, "lutq_mx_pack")
+    return MxPacked(dst, desc)
+
+
+def mx_matmul(x, p: MxPacked, *, dtype=None, path: str = "auto", out=None):
+    """y[M, N] = x . W^T with packed MX4 weights.
+
+    x fp16 or bf16 [M, K] (rows may be strided): lutq_mx_matmul, y in x's type.
+    x a (codes, scales) pair of mx_quantize: lutq_mx_matmul_mx, both operands
+    in 4 bits, y in ``dtype`` (bf16 by default)."""
+    if not isinstance(p, MxPacked):
+        raise TypeError("p must be an MxPacked (from mx_pack)")
+    if p.experts != 1:
+        raise ValueError(f"p holds {p.experts} experts, mx_matmul takes one matrix")
+    four = isinstance(x, (tuple, list))
+    if four:
+        xc, xs = _codes_of(x, "x")
+        if xc.dim() != 2:
+            raise ValueError("x codes must be [M, K/2]")
+        M, K = xc.shape[0], xc.shape[1] * 2
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if path != "auto":
+            raise ValueError("path chooses a kernel for 16-bit x only")
+    else:
+        ldx = _rows_of(x, "x", _HALF)
+        M, K = x.shape
+        if dtype is not None and dtype != x.dtype:
+            raise TypeError(f"y has the type of x ({x.dtype}), not {dtype}")
+        dtype = x.dtype
+    if dtype not in _HALF:
+        raise TypeError(f"dtype must be {' or '.join(str(d) for d in _HALF)}, got {dtype}")
+    if path not in _PATHS:
+        raise ValueError(f"path must be one of {sorted(_PATHS)}")
+    if K != p.K:
+        raise ValueError(f"x has K = {K}, the packed matrix K = {p.K}")
+    if out is not None:
+        _check(out, "out", dtype, shape=(M, p.N))
+    if four:
+        _on_device(("x codes", xc), ("x scales", xs), ("packed data", p.data), ("out", out))
+        dev = xc.device
+    else:
+        _on_device(("x", x), ("packed data", p.data), ("out", out))
+        dev = x.device
+    if out is None:
+        out = torch.empty((M, p.N), dtype=dtype, device=dev)
+    if four:
+        rc = _lib().lutq_mx_matmul_mx(xc.data_ptr(), xs.data_ptr(), p._ref, out.data_ptr(), _HALF[dtype], M,
+                                      p.N, K, _raw_stream(dev))
+    else:
+        rc = _lib().lutq_mx_matmul(x.data_ptr(), _HALF[dtype], ldx, p._ref, out.data_ptr(), M, p.N, K,
+                                   _PATHS[path], _raw_stream(dev))
+    if rc:
+        raise LutqError(rc, "lutq_mx_matmul")
+    return out
+
+
+class Routing:
+    """The experts of T tokens: ids int32 [T, k] (-1: none), weights fp32
+    [T, k], and the plan that groups the pairs t * k + j by expert."""
+
+    def __init__(self, ids, weights, plan, experts: int):
+        self.ids, self.weights, self.plan, self.experts = ids, weights, plan, experts
+
+    @property
+    def offsets(self):
+        """int32 [E + 1]: expert e's pairs are order[offsets[e]:offsets[e + 1]]."""
+        return self.plan[:self.experts + 1]
+
+    @property
+    def order(self):
+        """int32 [T * k]: the pairs by expert, rising within one; -1 past the last."""
+        return self.plan[self.experts + 1:self.experts + 1 + self.ids.numel()]
+
+
+def moe_route(logits, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
+              top_groups: int = 1, group_best: int = 1, renorm: bool = True,
+              scale: float = 1.0) -> Routing:
+    """lutq_moe_route: router logits [T, E] (fp32, fp16 or bf16; rows may be
+    strided) -> the k experts of each token, their weights and the plan."""
+    ld = _rows_of(logits, "logits", _TYPES)
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    T, E = logits.shape
+    if bias is not None:
+        _check(bias, "bias", torch.float32, shape=(E,))
+    _on_device(("logits", logits), ("bias", bias))
+    dev = logits.device
+    ints = _lib().lutq_moe_plan_ints(T, E, k)
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    plan = torch.empty(ints, dtype=torch.int32, device=dev)
+    o = MoeOptions(_SCORES[score], groups, top_groups, group_best, int(bool(renorm)), scale)
+    rc = _lib().lutq_moe_route(logits.data_ptr(), _TYPES[logits.dtype], ld,
+                               None if bias is None else bias.data_ptr(), T, E, k, ctypes.addressof(o),
+                               ids.data_ptr(), weights.data_ptr(), plan.data_ptr() or None,
+                               _raw_stream(dev))
+    if rc:
+        raise LutqError(rc, "lutq_moe_route")
+    return Routing(ids, weights, plan, E)
+
+
+def moe_plan(ids, weights, experts: int) -> Routing:
+    """lutq_moe_plan: the Routing of another router's ids int32 [T, k] and
+    weights fp32 [T, k]; an id outside [0, experts) stands for no expert."""
+    _check(ids, "ids", torch.int32)
+    if ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor [T, k]")
+    _check(weights, "weights", torch.float32, shape=ids.shape)
+    _on_device(("ids", ids), ("weights", weights))
+    T, k = ids.shape
+    plan = torch.empty(_lib().lutq_moe_plan_ints(T, experts, k), dtype=torch.int32, device=ids.device)
+    rc = _lib().lutq_moe_plan(ids.data_ptr(), T, experts, k, plan.data_ptr() or None, _raw_stream(ids.device))
+    if rc:
+        raise LutqError(rc, "lutq_moe_plan")
+    return Routing(ids, weights, plan, experts)
+
+
+def moe_mlp(x, gate_up: MxPacked, down: MxPacked, routing: Routing, *, out=None):
+    """lutq_moe_mlp: each token's experts, down . (silu(gate . x) * (up . x)),
+    summed with the routing's weights. x fp16 or bf16 [T, D]; gate_up packed
+    from [E, 2F, D] (gate rows, then up rows), down from [E, D, F]."""
+    ldx = _rows_of(x, "x", _HALF)
+    for name, p in (("gate_up", gate_up), ("down", down)):
+        if not isinstance(p, MxPacked):
+            raise TypeError(f"{name} must be an MxPacked (from mx_pack)")
+    if not isinstance(routing, Routing):
+        raise TypeError("routing must be a Routing (from moe_route or moe_plan)")
+    T, D = x.shape
+    E, F = gate_up.experts, down.K
+    if gate_up.K != D or down.N != D or gate_up.N != 2 * F or down.experts != E:
+        raise ValueError(f"gate_up [{E}, {gate_up.N}, {gate_up.K}] and down [{down.experts}, {down.N}, "
+                         f"{down.K}] do not fit x [{T}, {D}] and each other")
+    if routing.ids.shape[0] != T or routing.experts != E:
+        raise ValueError(f"routing of {routing.ids.shape[0]} tokens over {routing.experts} experts, "
+                         f"expected {T} over {E}")
+    if out is not None:
+        _check(out, "out", x.dtype, shape=(T, D))
+    _on_device(("x", x), ("gate_up data", gate_up.data), ("down data", down.data),
+               ("routing", routing.plan), ("out", out))
+    dev = x.device
+    k = routing.ids.shape[1]
+    lib = _lib()
+    nbytes = lib.lutq_moe_workspace_bytes(T, k, D, F)
+    space = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty((T, D), dtype=x.dtype, device=dev)
+    rc = lib.lutq_moe_mlp(x.data_ptr(), _HALF[x.dtype], ldx, gate_up._ref, down._ref,
+                          routing.ids.data_ptr(), routing.weights.data_ptr(), routing.plan.data_ptr(), T, k,
+                          space.data_ptr(), nbytes, out.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise LutqError(rc, "lutq_moe_mlp")
+    return out

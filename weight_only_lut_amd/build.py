@@ -18,7 +18,12 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [("lutq_api.cpp", []), ("lutq_layout.hip", []), ("lutq_quantize.hip", []),
            ("lutq_static.hip", []), ("lutq_peaks.hip", []),
            ("lutq_matmul.hip", ["-DLUTQ_MATMUL_BITS=2"]), ("lutq_matmul.hip", ["-DLUTQ_MATMUL_BITS=3"]),
-           ("lutq_matmul.hip", ["-DLUTQ_MATMUL_BITS=4"])]
+           ("lutq_matmul.hip", ["-DLUTQ_MATMUL_BITS=4"]),
+           # microscaled 4-bit and experts: the products once per activation type (1 fp16, 2 bf16)
+           ("lutq_mx_api.cpp", []), ("lutq_mx_quantize.hip", []), ("lutq_moe.hip", []),
+           ("lutq_mx_tile4.hip", []),
+           ("lutq_mx_stream.hip", ["-DLUTQ_MX_TYPE=1"]), ("lutq_mx_stream.hip", ["-DLUTQ_MX_TYPE=2"]),
+           ("lutq_mx_tile.hip", ["-DLUTQ_MX_TYPE=1"]), ("lutq_mx_tile.hip", ["-DLUTQ_MX_TYPE=2"])]
 LIB = os.path.join(HERE, "liblutq.so")
 # The same library with AddressSanitizer and UndefinedBehaviorSanitizer in
 # its host code only (argument validation, planning, scratch management);

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/lutq.h"
+#include "lutq_mx.h"
 #include "lutq_quant.h"
 
 namespace {
@@ -309,6 +310,11 @@ int run_matmul(const uint16_t* x, const lutq_matmul_item_t* items, int count, in
 }
 
 }  // namespace
+
+namespace lutq {
+int record_hip_error(hipError_t e) { return hip_fail(e); }
+int device_cu_count() { return cu_count(); }
+}  // namespace lutq
 
 extern "C" {
 

@@ -1,0 +1,531 @@
+// Routing to experts (gfx950): scores, the choice of k experts per token and
+// their weights; the plan that groups the (token, choice) pairs by expert; and
+// the sum of the experts' outputs per token.
+//
+// One wave routes a token: lane l holds the experts l, l + 64, ... in
+// registers, so that the logits are read once, coalesced, and a choice is a
+// wave maximum over order-preserving integer keys (four DPP steps, then scalar
+// code) and a ballot for the lowest expert that has it.
+//
+// The plan is a stable counting sort. Up to 1024 pairs one workgroup routes
+// and plans in a single launch, since there the launches are the time; beyond
+// that, segments of 2048 pairs are counted, the counts scanned, and each
+// segment places its pairs. Ranks come from ballots, never from the order in
+// which atomics happen to land.
+#include "lutq_mx_device.h"
+
+namespace lutq {
+namespace {
+
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+#define LUTQ_STEP(ctrl)                                                                   \
+  {                                                                                       \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true); \
+    v = v > o ? v : o;                                                                    \
+  }
+  LUTQ_STEP(0xB1)   // quad_perm [1,0,3,2]
+  LUTQ_STEP(0x4E)   // quad_perm [2,3,0,1]
+  LUTQ_STEP(0x141)  // row_half_mirror
+  LUTQ_STEP(0x140)  // row_mirror
+#undef LUTQ_STEP
+  return v;
+}
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = row_max_u32(v);
+  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+  const uint32_t x = a > b ? a : b, y = c > d ? c : d;
+  return x > y ? x : y;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Floats as unsigned integers in the same order; -0 counts as +0.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __builtin_bit_cast(float, (u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
+}
+
+__device__ __forceinline__ float load_logit(const RouteParams& p, long long at) {
+  if (p.dtype == kF32) return static_cast<const float*>(p.logits)[at];
+  const uint16_t h = static_cast<const uint16_t*>(p.logits)[at];
+  if (p.dtype == kF16) return f16_bits_to_f32(h);
+  return __builtin_bit_cast(float, (uint32_t)h << 16);
+}
+
+// The groups kept of the experts' keys in `keys` (LDS, -infinity for experts
+// never chosen), as a mask.
+__device__ uint64_t choose_groups(const RouteParams& p, const float* keys, int lane) {
+  const float kNone = -__builtin_inff();
+  int slots = 1;  // lanes per group
+  while (2 * slots * p.groups <= kWave) slots *= 2;
+  const int g = lane / slots, part = lane % slots, size = p.E / p.groups;
+  float best = kNone, second = kNone;
+  if (g < p.groups) {
+    for (int i = part; i < size; i += slots) {
+      const float v = keys[g * size + i];
+      second = fmaxf(second, fminf(best, v));
+      best = fmaxf(best, v);
+    }
+  }
+  for (int d = 1; d < slots; d <<= 1) {
+    const float ob = __shfl_xor(best, d), os = __shfl_xor(second, d);
+    second = fmaxf(fmaxf(second, os), fminf(best, ob));
+    best = fmaxf(best, ob);
+  }
+  const float rank = p.group_best == 2 ? best + second : best;
+  // 0 marks lanes that stand for no group; a group of -infinity ranks above
+  uint32_t key = g < p.groups && part == 0 ? ordered(rank) : 0;
+  uint64_t kept = 0;
+  for (int i = 0; i < p.top_groups; ++i) {
+    const uint32_t top = wave_max_u32(key);
+    const int at = __builtin_ctzll(__ballot(key == top));
+    kept |= 1ull << (at / slots);
+    if (lane == at) key = 0;
+  }
+  return kept;
+}
+
+// Routes token t with one wave; the ids also go to `ids_out` (LDS or global).
+// `keys` is E floats of LDS of this wave, used with groups only.
+template <int VPT>
+__device__ void route_token(const RouteParams& p, int t, int lane, float* keys, int32_t* ids_out) {
+  const float kNone = -__builtin_inff();
+  float logit[VPT], score[VPT];
+  uint32_t key[VPT];
+#pragma unroll
+  for (int s = 0; s < VPT; ++s) {
+    const int e = s * kWave + lane;
+    logit[s] = e < p.E ? load_logit(p, t * p.ld + e) : kNone;
+  }
+  bool bad = false;  // a NaN or +infinity in a softmax row
+  float top = kNone, total = 1.0f;
+  if (!p.sigmoid) {
+#pragma unroll
+    for (int s = 0; s < VPT; ++s) {
+      bad |= !(logit[s] < __builtin_inff());
+      top = fmaxf(top, logit[s]);
+    }
+    bad = __ballot(bad) != 0;
+    top = unordered(wave_max_u32(ordered(top)));
+    total = 0.0f;
+#pragma unroll
+    for (int s = 0; s < VPT; ++s) {
+      score[s] = logit[s] == kNone ? 0.0f : expf(logit[s] - top);
+      total += score[s];
+    }
+    total = wave_sum(total);
+  } else {
+#pragma unroll
+    for (int s = 0; s < VPT; ++s) score[s] = 1.0f / (1.0f + expf(-logit[s]));
+  }
+  const bool by_logit = !p.bias && (p.groups == 1 || p.group_best == 1);
+  float kf[VPT];
+#pragma unroll
+  for (int s = 0; s < VPT; ++s) {
+    const int e = s * kWave + lane;
+    float k = logit[s];
+    if (!by_logit && e < p.E) {
+      k = p.sigmoid ? score[s] : score[s] / total;
+      if (p.bias) k += p.bias[e];
+    }
+    if (logit[s] == kNone || k != k) k = kNone;
+    kf[s] = k;
+  }
+  uint64_t kept = ~0ull;
+  if (p.groups > 1) {
+#pragma unroll
+    for (int s = 0; s < VPT; ++s)
+      if (s * kWave + lane < p.E) keys[s * kWave + lane] = kf[s];
+    wave_lds_order();
+    kept = choose_groups(p, keys, lane);
+    wave_lds_order();
+  }
+  const int size = p.E / p.groups;
+#pragma unroll
+  for (int s = 0; s < VPT; ++s) {
+    key[s] = kf[s] == kNone ? 0u : ordered(kf[s]);
+    if (p.groups > 1 && !(kept >> ((s * kWave + lane) / size & 63) & 1)) key[s] = 0;
+  }
+  // choice j ends in lane j
+  int id = -1;
+  float mine = 0.0f;  // its logit (softmax) or score
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int s = 1; s < VPT; ++s) m = m > key[s] ? m : key[s];
+    m = wave_max_u32(m);
+    if (m == 0) break;
+    int at = -1;
+    float v = 0.0f;
+#pragma unroll
+    for (int s = 0; s < VPT; ++s) {
+      if (at < 0) {
+        const uint64_t b = __ballot(key[s] == m);
+        if (b) {
+          const int l = __builtin_ctzll(b);
+          at = s * kWave + l;
+          v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                  __builtin_bit_cast(int, p.sigmoid ? score[s] : logit[s]), l));
+          if (lane == l) key[s] = 0;
+        }
+      }
+    }
+    if (lane == j) {
+      id = at;
+      mine = v;
+    }
+  }
+  float w = 0.0f;
+  if (p.sigmoid) {
+    w = id >= 0 ? mine : 0.0f;
+    if (p.renorm) w = w / (wave_sum(w) + 1e-20f);
+  } else {
+    // with renorm the chosen are measured from the first, the largest unless
+    // a bias reordered them
+    const float ref = p.renorm ? unordered(wave_max_u32(id >= 0 ? ordered(mine) : 0u)) : top;
+    w = id >= 0 ? expf(mine - ref) : 0.0f;
+    const float sum = p.renorm ? wave_sum(w) : total;
+    w = id < 0 ? 0.0f : bad ? __builtin_nanf("") : w / sum;
+  }
+  if (lane < p.k) {
+    const size_t at = (size_t)t * p.k + lane;
+    p.ids[at] = id;
+    p.weights[at] = id >= 0 ? w * p.scale : 0.0f;
+    if (ids_out) ids_out[lane] = id;
+  }
+}
+
+constexpr int kRouteWaves = 4;
+
+template <int VPT>
+__global__ __launch_bounds__(kRouteWaves * 64) void moe_route_kernel(RouteParams p) {
+  __shared__ float keys[kRouteWaves][VPT * kWave];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * kRouteWaves + wave;
+  if (t < p.T) route_token<VPT>(p, t, lane, keys[wave], nullptr);
+}
+
+// Exclusive prefix sums of v[0 .. n) in place over a workgroup of THREADS;
+// returns the total. `tmp` holds THREADS / 64 ints.
+template <int THREADS>
+__device__ int block_scan(int* v, int n, int* tmp) {
+  constexpr int kWaves = THREADS / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (n + THREADS - 1) / THREADS, b = tid * per;
+  int sum = 0;
+  for (int i = 0; i < per; ++i)
+    if (b + i < n) sum += v[b + i];
+  int inc = sum;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) tmp[wave] = inc;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < wave) before += tmp[i];
+    total += tmp[i];
+  }
+  int run = before + inc - sum;
+  for (int i = 0; i < per; ++i)
+    if (b + i < n) {
+      const int x = v[b + i];
+      v[b + i] = run;
+      run += x;
+    }
+  __syncthreads();
+  return total;
+}
+
+// Offsets and row tiles from the experts' counts in LDS (`cnt`, which become
+// the offsets). `aux` holds E ints, `tmp` THREADS / 64.
+template <int THREADS>
+__device__ void write_offsets_and_tiles(int* cnt, int* aux, int* tmp, int E, int rows, int32_t* plan,
+                                        int32_t* tiles) {
+  for (int e = threadIdx.x; e < E; e += THREADS) aux[e] = (cnt[e] + rows - 1) / rows;
+  __syncthreads();
+  const int total = block_scan<THREADS>(cnt, E, tmp);
+  const int ntiles = block_scan<THREADS>(aux, E, tmp);
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    const int b = cnt[e], n = (e + 1 < E ? cnt[e + 1] : total) - b;
+    plan[e] = b;
+    int32_t* out = tiles + 4 + 4 * (size_t)aux[e];
+    for (int i = 0; i < n; i += rows, out += 4) {
+      out[0] = e;
+      out[1] = b + i;
+      out[2] = n - i < rows ? n - i : rows;
+      out[3] = 0;
+    }
+  }
+  if (threadIdx.x == 0) {
+    plan[E] = total;
+    tiles[0] = ntiles;
+  }
+}
+
+// Places the pairs [b, b + n) of this workgroup: run[wave][e] holds each
+// wave's counts on entry, the first position of expert e's pairs `base(e)`.
+template <int WAVES, class Base, class Id>
+__device__ void place_pairs(int* run, int E, int b, int n, Base base, Id id_of, int32_t* order) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int e = threadIdx.x; e < E; e += WAVES * 64) {
+    int at = base(e);
+    for (int w = 0; w < WAVES; ++w) {
+      const int c = run[w * E + e];
+      run[w * E + e] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  int bits = 0;
+  while ((1 << bits) < E) ++bits;
+  const int per = (n + WAVES * 64 - 1) / (WAVES * 64) * 64;
+  const int w0 = wave * per, w1 = w0 + per < n ? w0 + per : n;
+  int* mine = run + wave * E;
+  for (int i = w0; i < w1; i += 64) {
+    const int at = i + lane;
+    const int e = at < w1 ? id_of(b + at) : -1;
+    const bool live = (unsigned)e < (unsigned)E;
+    uint64_t same = __ballot(live);  // lanes with this lane's expert
+    for (int k = 0; k < bits; ++k) {
+      const uint64_t set = __ballot(live && (e >> k & 1));
+      same &= (e >> k & 1) ? set : ~set;
+    }
+    const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
+    int first = 0;
+    if (live) first = mine[e];
+    wave_lds_order();
+    if (live) {
+      order[first + before] = b + at;
+      if (before == 0) mine[e] = first + __builtin_popcountll(same);
+    }
+    wave_lds_order();
+  }
+}
+
+template <int WAVES, class Id>
+__device__ void count_pairs(int* run, int E, int b, int n, Id id_of) {
+  for (int i = threadIdx.x; i < WAVES * E; i += WAVES * 64) run[i] = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (n + WAVES * 64 - 1) / (WAVES * 64) * 64;
+  const int w0 = wave * per, w1 = w0 + per < n ? w0 + per : n;
+  for (int i = w0 + lane; i < w1; i += 64) {
+    const int e = id_of(b + i);
+    if ((unsigned)e < (unsigned)E) atomicAdd(&run[wave * E + e], 1);
+  }
+  __syncthreads();
+}
+
+constexpr int kSmallWaves = 16;
+
+// Few pairs: one workgroup routes (unless VPT is 0) and plans.
+template <int VPT>
+__global__ __launch_bounds__(kSmallWaves * 64) void moe_small_kernel(RouteParams p, MoePlanLayout l,
+                                                                      int tile_rows) {
+  extern __shared__ int lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = p.T * p.k, E = p.E;
+  int* run = lds;                        // [kSmallWaves][E]
+  int* cnt = run + kSmallWaves * E;      // [E]
+  int* aux = cnt + E;                    // [E]
+  int* tmp = aux + E;                    // [kSmallWaves]
+  int32_t* ids = tmp + kSmallWaves;      // [n]
+  if constexpr (VPT > 0) {
+    float* keys = reinterpret_cast<float*>(run) + wave * E;
+    for (int t = wave; t < p.T; t += kSmallWaves)
+      route_token<VPT>(p, t, lane, keys, ids + t * p.k);
+  } else {
+    for (int i = threadIdx.x; i < n; i += kSmallWaves * 64) ids[i] = p.ids[i];
+  }
+  if (!p.plan) return;
+  __syncthreads();
+  const auto id_of = [&](int i) { return ids[i]; };
+  count_pairs<kSmallWaves>(run, E, 0, n, id_of);
+  for (int e = threadIdx.x; e < E; e += kSmallWaves * 64) {
+    int c = 0;
+    for (int w = 0; w < kSmallWaves; ++w) c += run[w * E + e];
+    cnt[e] = c;
+  }
+  __syncthreads();
+  write_offsets_and_tiles<kSmallWaves * 64>(cnt, aux, tmp, E, tile_rows, p.plan, p.plan + l.tiles);
+  int32_t* order = p.plan + l.order;
+  int live = 0;  // as plan[E]
+  for (int w = 0; w < kSmallWaves; ++w) live += run[w * E + E - 1];
+  live += cnt[E - 1];
+  __syncthreads();
+  place_pairs<kSmallWaves>(run, E, 0, n, [&](int e) { return cnt[e]; }, id_of, order);
+  for (int i = live + threadIdx.x; i < n; i += kSmallWaves * 64) order[i] = -1;
+}
+
+constexpr int kSegWaves = 4;
+
+__global__ __launch_bounds__(kSegWaves * 64) void moe_count_kernel(const int32_t* ids, int pairs, int E,
+                                                                    int32_t* counts) {
+  extern __shared__ int lds[];
+  const int b = blockIdx.x * kPlanSegment, n = pairs - b < kPlanSegment ? pairs - b : kPlanSegment;
+  count_pairs<kSegWaves>(lds, E, b, n, [&](int i) { return ids[i]; });
+  for (int e = threadIdx.x; e < E; e += kSegWaves * 64) {
+    int c = 0;
+    for (int w = 0; w < kSegWaves; ++w) c += lds[w * E + e];
+    counts[(size_t)blockIdx.x * E + e] = c;
+  }
+}
+
+// Per expert the counts become what earlier segments hold; then the offsets
+// and row tiles.
+__global__ __launch_bounds__(1024) void moe_scan_kernel(int32_t* counts, int segments, int E,
+                                                         int tile_rows, int32_t* plan, int32_t* tiles) {
+  extern __shared__ int lds[];
+  int* cnt = lds;
+  int* aux = cnt + E;
+  int* tmp = aux + E;
+  for (int e = threadIdx.x; e < E; e += 1024) {
+    int run = 0;
+    int s = 0;
+    for (; s + 8 <= segments; s += 8) {  // the loads of eight segments at once
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = counts[(size_t)(s + i) * E + e];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        counts[(size_t)(s + i) * E + e] = run;
+        run += c[i];
+      }
+    }
+    for (; s < segments; ++s) {
+      const int c = counts[(size_t)s * E + e];
+      counts[(size_t)s * E + e] = run;
+      run += c;
+    }
+    cnt[e] = run;
+  }
+  __syncthreads();
+  write_offsets_and_tiles<1024>(cnt, aux, tmp, E, tile_rows, plan, tiles);
+}
+
+__global__ __launch_bounds__(kSegWaves * 64) void moe_place_kernel(const int32_t* ids, int pairs, int E,
+                                                                    const int32_t* counts,
+                                                                    const int32_t* plan, int32_t* order) {
+  extern __shared__ int lds[];
+  const int b = blockIdx.x * kPlanSegment, n = pairs - b < kPlanSegment ? pairs - b : kPlanSegment;
+  const auto id_of = [&](int i) { return ids[i]; };
+  count_pairs<kSegWaves>(lds, E, b, n, id_of);
+  place_pairs<kSegWaves>(lds, E, b, n,
+                         [&](int e) { return plan[e] + counts[(size_t)blockIdx.x * E + e]; }, id_of,
+                         order);
+  // positions past the last pair
+  for (int i = b + threadIdx.x; i < b + n; i += kSegWaves * 64)
+    if (i >= plan[E]) order[i] = -1;
+}
+
+// y[t] = the pair outputs of token t summed in the order of j, in fp32.
+template <int DT>
+__global__ __launch_bounds__(256) void moe_combine_kernel(const float* pairs, const int32_t* ids,
+                                                           uint16_t* y, int k, int D, int E) {
+  const int t = blockIdx.y;
+  const int n = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
+  if (n >= D) return;
+  f32x4 sum = {0, 0, 0, 0};
+  for (int j = 0; j < k; ++j) {
+    const int id = ids[(size_t)t * k + j];
+    if ((unsigned)id >= (unsigned)E) continue;
+    const float* row = pairs + ((size_t)t * k + j) * D + n;
+    if ((D & 3) == 0) {
+      sum += *reinterpret_cast<const f32x4*>(row);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < D) sum[i] += row[i];
+    }
+  }
+  store4<DT>(y + (size_t)t * D, n, D, sum);
+}
+
+size_t small_lds(int E, int n) {
+  return sizeof(int) * ((size_t)(kSmallWaves + 2) * E + kSmallWaves + n);
+}
+
+// One workgroup plans, within the LDS that needs no opting in.
+bool small_plan(int E, long long pairs) {
+  return pairs <= kPlanSmallPairs && small_lds(E, (int)pairs) <= 64u * 1024;
+}
+
+template <int VPT>
+hipError_t route(const RouteParams& p, bool small, hipStream_t s) {
+  if (small) {
+    const MoePlanLayout l = moe_plan_layout(p.T, p.E, p.k);
+    moe_small_kernel<VPT><<<1, kSmallWaves * 64, small_lds(p.E, p.T * p.k), s>>>(
+        p, l, moe_tile_rows((long long)p.T * p.k, p.E));
+  } else {
+    moe_route_kernel<VPT><<<(p.T + kRouteWaves - 1) / kRouteWaves, kRouteWaves * 64, 0, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, hipStream_t s) {
+  const MoePlanLayout l = moe_plan_layout(T, E, k);
+  const int pairs = T * k, rows = moe_tile_rows(pairs, E);
+  if (small_plan(E, pairs)) {
+    RouteParams p = {};
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.ids = const_cast<int32_t*>(ids);
+    p.plan = plan;
+    moe_small_kernel<0><<<1, kSmallWaves * 64, small_lds(E, pairs), s>>>(p, l, rows);
+    return hipGetLastError();
+  }
+  int32_t* counts = plan + l.counts;
+  const size_t lds = sizeof(int) * kSegWaves * E;
+  moe_count_kernel<<<l.segments, kSegWaves * 64, lds, s>>>(ids, pairs, E, counts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  moe_scan_kernel<<<1, 1024, sizeof(int) * (2 * E + 16), s>>>(counts, l.segments, E, rows, plan,
+                                                              plan + l.tiles);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  moe_place_kernel<<<l.segments, kSegWaves * 64, lds, s>>>(ids, pairs, E, counts, plan, plan + l.order);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route(const RouteParams& p, hipStream_t s) {
+  const bool small = p.T <= kPlanSmallTokens && small_plan(p.E, (long long)p.T * p.k);
+  hipError_t e;
+  if (p.E <= 64) e = route<1>(p, small, s);
+  else if (p.E <= 128) e = route<2>(p, small, s);
+  else if (p.E <= 256) e = route<4>(p, small, s);
+  else if (p.E <= 512) e = route<8>(p, small, s);
+  else e = route<16>(p, small, s);
+  if (e != hipSuccess || small || !p.plan) return e;
+  return launch_moe_plan(p.ids, p.T, p.E, p.k, p.plan, s);
+}
+
+hipError_t launch_moe_combine(const float* pairs, const int32_t* ids, void* y, int dtype, int T,
+                              int k, int D, int E, hipStream_t s) {
+  const unsigned gx = (unsigned)((D + 1023) / 1024);
+  for (int t0 = 0; t0 < T; t0 += 65535) {  // grid.y
+    const dim3 g(gx, (unsigned)(T - t0 < 65535 ? T - t0 : 65535));
+    const float* pr = pairs + (size_t)t0 * k * D;
+    const int32_t* ir = ids + (size_t)t0 * k;
+    uint16_t* yr = static_cast<uint16_t*>(y) + (size_t)t0 * D;
+    if (dtype == kF16) moe_combine_kernel<kF16><<<g, 256, 0, s>>>(pr, ir, yr, k, D, E);
+    else moe_combine_kernel<kBf16><<<g, 256, 0, s>>>(pr, ir, yr, k, D, E);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace lutq

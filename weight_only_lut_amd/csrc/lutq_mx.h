@@ -1,0 +1,149 @@
+// Internal interface of the microscaled 4-bit (MX4) and expert kernels: the
+// packed layout's geometry, kernel parameters and launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lutq_internal.h"
+
+namespace lutq {
+
+// Records a failed HIP call for lutq_last_hip_error; returns LUTQ_EHIP.
+int record_hip_error(hipError_t e);
+// Compute units of the current device (cached per device).
+int device_cu_count();
+
+constexpr int kMxBlock = 32;     // values per scale
+constexpr int kMxSlotBytes = 16; // a block's codes
+constexpr int kMxBlockBytes = kWave * kMxSlotBytes;  // one tile x chunk of codes: 1 KiB
+
+enum MxType { kF32 = 0, kF16 = 1, kBf16 = 2 };
+
+// Where the parts of packed weights lie in their buffer (see lutq_mx.h).
+struct MxLayout {
+  int ntile, nchunk, nquad;
+  size_t code_bytes, scale_bytes, row_bytes;  // per expert
+  size_t bytes(int experts) const { return (code_bytes + scale_bytes + row_bytes) * (size_t)experts; }
+};
+inline MxLayout mx_layout(int N, int K) {
+  MxLayout l;
+  l.ntile = (int)(((long long)N + kTileRows - 1) / kTileRows);
+  l.nchunk = (K + kChunk - 1) / kChunk;
+  l.nquad = (l.nchunk + 3) / 4;
+  l.code_bytes = (size_t)l.ntile * l.nchunk * kMxBlockBytes;
+  l.scale_bytes = (size_t)l.ntile * l.nquad * kWave * 4;
+  l.row_bytes = (size_t)l.ntile * kTileRows * sizeof(float);
+  return l;
+}
+
+// Packed weights as a kernel sees them.
+struct MxWeights {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* rows;
+  size_t expert_codes, expert_scales, expert_rows;  // strides: bytes, bytes, floats
+  int N, K, ntile, nchunk, nquad;
+};
+
+// What a product kernel does with rows: see lutq_mx_matmul.hip.
+enum MxMode {
+  kMxDense = 0,     // row m of x -> row m of y
+  kMxUp = 1,        // experts' gate and up rows: sorted pair p reads x[order[p] / k], writes h[p]
+  kMxDown = 2,      // experts' down rows: h[p] -> fp32 pair output order[p], times its weight
+  kMxUpPair = 3,    // as kMxUp for pair p itself (no order), one pair per workgroup
+  kMxDownToken = 4  // all pairs of a token: h[t * k + j] -> y[t]
+};
+
+struct MxParams {
+  const void* x;         // 16-bit rows (or 4-bit codes with xscales)
+  const uint8_t* xscales;
+  long long ldx;         // elements (bytes for 4-bit codes)
+  MxWeights w;
+  void* y;               // dense: 16-bit [M][N]; up: h [pairs][F], fp32 (stream) or 16-bit
+                         // (tile); down: fp32 [pairs][D]; down-token: 16-bit [T][D]
+  int M;                 // dense: rows
+  // grouped
+  const int32_t* ids;
+  const float* weights;
+  const int32_t* order;
+  const int32_t* tiles;  // [0] the count, then {expert, first position, rows, 0} from [4]
+  int max_tiles;         // entries at most (the grid)
+  int pairs, topk, experts;
+};
+
+// Rows of a grouped row tile, by the average number of pairs per expert:
+// what the plan cuts and the product kernels are compiled for.
+int moe_tile_rows(long long pairs, int experts);
+// Row tiles at most: every expert ends with at most one partial tile.
+inline long long moe_max_tiles(long long pairs, int experts, int rows) {
+  const long long e = experts < pairs ? experts : pairs;
+  return pairs / rows + e;
+}
+// The pairs up to which the experts' products run pair by pair, without a plan.
+bool moe_direct(long long pairs, int topk, int experts);
+
+// Segments the plan of many pairs is built in.
+constexpr int kPlanSegment = 2048;
+constexpr int kPlanSmallPairs = 1024;  // up to here one workgroup routes and plans
+constexpr int kPlanSmallTokens = 64;
+
+// Integer offsets of a plan's parts.
+struct MoePlanLayout {
+  long long order, tiles, counts, total;
+  int max_tiles, segments;
+};
+inline MoePlanLayout moe_plan_layout(int T, int E, int k) {
+  MoePlanLayout l;
+  const long long pairs = (long long)T * k;
+  l.order = E + 1;
+  l.tiles = (l.order + pairs + 3) / 4 * 4;
+  l.max_tiles = (int)moe_max_tiles(pairs, E, moe_tile_rows(pairs, E));
+  l.counts = l.tiles + 4 + 4LL * l.max_tiles;
+  l.segments = (int)((pairs + kPlanSegment - 1) / kPlanSegment);
+  l.total = l.counts + (long long)l.segments * E;
+  return l;
+}
+
+struct RouteParams {
+  const void* logits;
+  int dtype;
+  long long ld;
+  const float* bias;
+  int T, E, k, sigmoid, groups, top_groups, group_best, renorm;
+  float scale;
+  int32_t* ids;
+  float* weights;
+  int32_t* plan;  // or null
+};
+
+hipError_t launch_mx_quantize(const void* x, int dtype, int rows, int K, long long ldx, int rule,
+                              uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype,
+                                long long values, void* x, hipStream_t s);
+hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N, int K,
+                          void* dst, hipStream_t s);
+// Sets n 16-bit values to zero.
+inline hipError_t launch_mx_zero(void* y, long long n, hipStream_t s) {
+  return launch_fill_u16(static_cast<uint16_t*>(y), n, 0, s);
+}
+// dtype: kF16 or kBf16 of x, h and y; compiled once for each.
+template <int DT> hipError_t mx_stream(const MxParams& p, int mode, int cus, hipStream_t s);
+template <int DT> hipError_t mx_tile(const MxParams& p, int mode, int cus, hipStream_t s);
+template <> hipError_t mx_stream<kF16>(const MxParams& p, int mode, int cus, hipStream_t s);
+template <> hipError_t mx_stream<kBf16>(const MxParams& p, int mode, int cus, hipStream_t s);
+template <> hipError_t mx_tile<kF16>(const MxParams& p, int mode, int cus, hipStream_t s);
+template <> hipError_t mx_tile<kBf16>(const MxParams& p, int mode, int cus, hipStream_t s);
+inline hipError_t launch_mx_stream(const MxParams& p, int dtype, int mode, int cus, hipStream_t s) {
+  return dtype == kF16 ? mx_stream<kF16>(p, mode, cus, s) : mx_stream<kBf16>(p, mode, cus, s);
+}
+inline hipError_t launch_mx_tile(const MxParams& p, int dtype, int mode, int cus, hipStream_t s) {
+  return dtype == kF16 ? mx_tile<kF16>(p, mode, cus, s) : mx_tile<kBf16>(p, mode, cus, s);
+}
+hipError_t launch_mx_tile4(const MxParams& p, int dtype, int cus, hipStream_t s);
+hipError_t launch_moe_route(const RouteParams& p, hipStream_t s);
+hipError_t launch_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, hipStream_t s);
+hipError_t launch_moe_combine(const float* pairs, const int32_t* ids, void* y, int dtype, int T,
+                              int k, int D, int E, hipStream_t s);
+
+}  // namespace lutq

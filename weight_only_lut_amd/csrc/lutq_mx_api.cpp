@@ -1,0 +1,333 @@
+// C-ABI host side of the microscaled 4-bit and expert operators: argument
+// validation and launches. Nothing is allocated and no HIP call comes before
+// the arguments are checked.
+#include <cstring>
+
+#include "../../include/lutq_moe.h"
+#include "lutq_mx.h"
+
+namespace lutq {
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+static_assert(LUTQ_WEIGHT_F32 == kF32 && LUTQ_WEIGHT_F16 == kF16 && LUTQ_WEIGHT_BF16 == kBf16,
+              "element types");
+static_assert(LUTQ_MX_BLOCK == kMxBlock, "block size");
+
+int elem_bytes(int dtype) { return dtype == kF32 ? 4 : 2; }
+
+bool any_type(int dtype) { return dtype == kF32 || dtype == kF16 || dtype == kBf16; }
+bool half_type(int dtype) { return dtype == kF16 || dtype == kBf16; }
+
+int check_rows(long long rows, int K) {
+  if (rows < 0 || K < 0) return LUTQ_EINVAL;
+  if (K % kMxBlock) return LUTQ_EGROUP;
+  if (K > LUTQ_MAX_K || rows * K > LUTQ_MAX_NK) return LUTQ_EUNSUPPORTED;
+  return LUTQ_OK;
+}
+
+int check_weights(int experts, int N, int K) {
+  if (experts < 1 || N < 0 || K < 0) return LUTQ_EINVAL;
+  if (K % kMxBlock) return LUTQ_EGROUP;
+  if (experts > LUTQ_MX_MAX_EXPERTS || N > LUTQ_MAX_N || K > LUTQ_MAX_K ||
+      (long long)N * K > LUTQ_MAX_NK / experts)
+    return LUTQ_EUNSUPPORTED;
+  return LUTQ_OK;
+}
+
+int check_packed(const lutq_mx_packed_t* p) {
+  if (!p) return LUTQ_EINVAL;
+  if (p->magic != LUTQ_MX_MAGIC || p->version != LUTQ_MX_LAYOUT_VERSION) return LUTQ_EMISMATCH;
+  const int rc = check_weights(p->experts, p->N, p->K);
+  if (rc) return rc;
+  if (p->nbytes != lutq_mx_packed_bytes(p->experts, p->N, p->K)) return LUTQ_EMISMATCH;
+  if (p->nbytes && !p->data) return LUTQ_EINVAL;
+  if (!aligned(p->data, 16)) return LUTQ_EALIGN;
+  return LUTQ_OK;
+}
+
+MxWeights weights_of(const lutq_mx_packed_t* p) {
+  const MxLayout l = mx_layout(p->N, p->K);
+  MxWeights w;
+  w.codes = static_cast<const uint8_t*>(p->data);
+  w.scales = w.codes + l.code_bytes * p->experts;
+  w.rows = reinterpret_cast<const float*>(w.scales + l.scale_bytes * p->experts);
+  w.expert_codes = l.code_bytes;
+  w.expert_scales = l.scale_bytes;
+  w.expert_rows = l.row_bytes / sizeof(float);
+  w.N = p->N;
+  w.K = p->K;
+  w.ntile = l.ntile;
+  w.nchunk = l.nchunk;
+  w.nquad = l.nquad;
+  return w;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? LUTQ_OK : record_hip_error(e); }
+
+// Sizes of a routing; T, E, k in range after this.
+int check_route(int T, int E, int k) {
+  if (T < 0 || E < 1 || k < 1 || k > E) return LUTQ_EINVAL;
+  if (E > LUTQ_MOE_MAX_EXPERTS || k > LUTQ_MOE_MAX_TOPK || (long long)T * k > LUTQ_MOE_MAX_PAIRS)
+    return LUTQ_EUNSUPPORTED;
+  return LUTQ_OK;
+}
+
+// Whether a launch over row tiles x column tiles of at least 64 fits a grid.
+bool tiles_fit(long long row_tiles, long long N) { return row_tiles * ((N + 63) / 64) <= 0x7FFFFFFF; }
+
+// Rows of a stream launch above which the tiled kernel is faster.
+constexpr int kStreamRows = 64;
+
+}  // namespace
+
+int moe_tile_rows(long long pairs, int experts) { return pairs > 16LL * experts ? 128 : 16; }
+
+bool moe_direct(long long pairs, int topk, int experts) {
+  return topk <= 16 && pairs <= 64;
+}
+
+}  // namespace lutq
+
+using namespace lutq;
+
+extern "C" {
+
+int lutq_mx_quantize(const void* x, int dtype, int rows, int K, long long ldx, int rule,
+                     uint8_t* codes, uint8_t* scales, void* stream) {
+  const int rc = check_rows(rows, K);
+  if (rc) return rc;
+  if (!any_type(dtype) || (rule != LUTQ_MX_FLOOR && rule != LUTQ_MX_CEIL)) return LUTQ_EINVAL;
+  if (rows == 0 || K == 0) return LUTQ_OK;
+  if (!x || !codes || !scales || ldx < K) return LUTQ_EINVAL;
+  if (!aligned(x, 16) || ldx * elem_bytes(dtype) % 16 || !aligned(codes, 4)) return LUTQ_EALIGN;
+  return status(launch_mx_quantize(x, dtype, rows, K, ldx, rule, codes, scales, (hipStream_t)stream));
+}
+
+int lutq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype, int rows, int K,
+                       void* x, void* stream) {
+  const int rc = check_rows(rows, K);
+  if (rc) return rc;
+  if (!any_type(dtype)) return LUTQ_EINVAL;
+  if (rows == 0 || K == 0) return LUTQ_OK;
+  if (!x || !codes || !scales) return LUTQ_EINVAL;
+  if (!aligned(x, 16) || !aligned(codes, 4)) return LUTQ_EALIGN;
+  return status(launch_mx_dequantize(codes, scales, dtype, (long long)rows * K, x, (hipStream_t)stream));
+}
+
+size_t lutq_mx_packed_bytes(int experts, int N, int K) {
+  if (check_weights(experts, N, K) || N == 0 || K == 0) return 0;
+  return mx_layout(N, K).bytes(experts);
+}
+
+int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N, int K, void* dst,
+                 size_t dst_bytes, lutq_mx_packed_t* out, void* stream) {
+  if (!out) return LUTQ_EINVAL;
+  const int rc = check_weights(experts, N, K);
+  if (rc) return rc;
+  const size_t need = lutq_mx_packed_bytes(experts, N, K);
+  if (need) {
+    if (!codes || !scales || !dst) return LUTQ_EINVAL;
+    if (!aligned(codes, 16) || !aligned(dst, 16)) return LUTQ_EALIGN;
+    if (dst_bytes < need) return LUTQ_ESIZE;
+    const size_t values = (size_t)experts * N * K;
+    const char* d = static_cast<const char*>(dst);
+    const auto overlap = [&](const uint8_t* p, size_t n) {
+      const char* a = reinterpret_cast<const char*>(p);
+      return a < d + need && d < a + n;
+    };
+    if (overlap(codes, values / 2) || overlap(scales, values / kMxBlock)) return LUTQ_EINVAL;
+    const hipError_t e = launch_mx_pack(codes, scales, experts, N, K, dst, (hipStream_t)stream);
+    if (e != hipSuccess) return record_hip_error(e);
+  }
+  lutq_mx_packed_t p;
+  std::memset(&p, 0, sizeof p);
+  p.magic = LUTQ_MX_MAGIC;
+  p.version = LUTQ_MX_LAYOUT_VERSION;
+  p.experts = experts;
+  p.N = N;
+  p.K = K;
+  p.nbytes = need;
+  p.data = need ? dst : nullptr;
+  *out = p;
+  return LUTQ_OK;
+}
+
+int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,
+                   int M, int N, int K, int path, void* stream) {
+  int rc = check_packed(packed);
+  if (rc) return rc;
+  if (M < 0 || N < 0 || K < 0 || !half_type(dtype) || path < LUTQ_MX_PATH_AUTO ||
+      path > LUTQ_MX_PATH_TILE)
+    return LUTQ_EINVAL;
+  if (packed->experts != 1 || N != packed->N || K != packed->K) return LUTQ_EMISMATCH;
+  if (M == 0 || N == 0) return LUTQ_OK;
+  if (!y) return LUTQ_EINVAL;
+  if (!aligned(y, 8)) return LUTQ_EALIGN;
+  if (!tiles_fit((M + 63LL) / 64, N)) return LUTQ_EUNSUPPORTED;
+  const hipStream_t s = (hipStream_t)stream;
+  if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
+  if (!x || ldx < K) return LUTQ_EINVAL;
+  if (!aligned(x, 16) || ldx % 8) return LUTQ_EALIGN;
+  MxParams p = {};
+  p.x = x;
+  p.ldx = ldx;
+  p.w = weights_of(packed);
+  p.y = y;
+  p.M = M;
+  if (path == LUTQ_MX_PATH_AUTO) path = M <= kStreamRows ? LUTQ_MX_PATH_STREAM : LUTQ_MX_PATH_TILE;
+  return status(path == LUTQ_MX_PATH_STREAM ? launch_mx_stream(p, dtype, kMxDense, device_cu_count(), s)
+                                            : launch_mx_tile(p, dtype, kMxDense, device_cu_count(), s));
+}
+
+int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
+                      void* y, int dtype, int M, int N, int K, void* stream) {
+  int rc = check_packed(packed);
+  if (rc) return rc;
+  if (M < 0 || N < 0 || K < 0 || !half_type(dtype)) return LUTQ_EINVAL;
+  if (packed->experts != 1 || N != packed->N || K != packed->K) return LUTQ_EMISMATCH;
+  if (M == 0 || N == 0) return LUTQ_OK;
+  if (!y) return LUTQ_EINVAL;
+  if (!aligned(y, 8)) return LUTQ_EALIGN;
+  if (!tiles_fit((M + 63LL) / 64, N)) return LUTQ_EUNSUPPORTED;
+  const hipStream_t s = (hipStream_t)stream;
+  if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
+  if (!xcodes || !xscales) return LUTQ_EINVAL;
+  if (!aligned(xcodes, 16)) return LUTQ_EALIGN;
+  MxParams p = {};
+  p.x = xcodes;
+  p.xscales = xscales;
+  p.ldx = K / 2;
+  p.w = weights_of(packed);
+  p.y = y;
+  p.M = M;
+  return status(launch_mx_tile4(p, dtype, device_cu_count(), s));
+}
+
+size_t lutq_moe_plan_ints(int T, int E, int k) {
+  if (check_route(T, E, k)) return 0;
+  return (size_t)moe_plan_layout(T, E, k).total;
+}
+
+int lutq_moe_route(const void* logits, int dtype, long long ld, const float* bias, int T, int E,
+                   int k, const lutq_moe_options_t* opts, int32_t* ids, float* weights,
+                   int32_t* plan, void* stream) {
+  const int rc = check_route(T, E, k);
+  if (rc) return rc;
+  if (!any_type(dtype)) return LUTQ_EINVAL;
+  lutq_moe_options_t o = {LUTQ_MOE_SOFTMAX, 1, 1, 1, 1, 1.0f, {0, 0}};
+  if (opts) o = *opts;
+  if ((o.score != LUTQ_MOE_SOFTMAX && o.score != LUTQ_MOE_SIGMOID) || o.groups < 1 ||
+      E % o.groups || o.top_groups < 1 || o.top_groups > o.groups || o.group_best < 1 ||
+      o.group_best > 2 || (o.groups > 1 && E / o.groups < o.group_best) || o.renorm < 0 ||
+      o.renorm > 1 || !(o.scale == o.scale) || o.reserved[0] || o.reserved[1])
+    return LUTQ_EINVAL;
+  if (o.groups > LUTQ_MOE_MAX_GROUPS) return LUTQ_EUNSUPPORTED;
+  const hipStream_t s = (hipStream_t)stream;
+  if (plan && !aligned(plan, 4)) return LUTQ_EALIGN;
+  if (T == 0) return plan ? status(launch_moe_plan(nullptr, 0, E, k, plan, s)) : LUTQ_OK;
+  if (!logits || !ids || !weights || ld < E) return LUTQ_EINVAL;
+  if (!aligned(logits, elem_bytes(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return LUTQ_EALIGN;
+  RouteParams p = {};
+  p.logits = logits;
+  p.dtype = dtype;
+  p.ld = ld;
+  p.bias = bias;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.sigmoid = o.score == LUTQ_MOE_SIGMOID;
+  p.groups = o.groups;
+  p.top_groups = o.top_groups;
+  p.group_best = o.group_best;
+  p.renorm = o.renorm;
+  p.scale = o.scale;
+  p.ids = ids;
+  p.weights = weights;
+  p.plan = plan;
+  return status(launch_moe_route(p, s));
+}
+
+int lutq_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, void* stream) {
+  const int rc = check_route(T, E, k);
+  if (rc) return rc;
+  if (!plan || (T > 0 && !ids)) return LUTQ_EINVAL;
+  if (!aligned(plan, 4) || !aligned(ids, 4)) return LUTQ_EALIGN;
+  return status(launch_moe_plan(ids, T, E, k, plan, (hipStream_t)stream));
+}
+
+// The workspace: h [pairs][F], sized for fp32, then fp32 [pairs][D] of the
+// pairs' outputs (not used where one workgroup sums a token's experts itself).
+size_t lutq_moe_workspace_bytes(int T, int k, int D, int F) {
+  if (T < 0 || k < 1 || k > LUTQ_MOE_MAX_TOPK || D < 0 || F < 0) return 0;
+  const size_t pairs = (size_t)T * k;
+  return (pairs * F + pairs * D) * sizeof(float);
+}
+
+int lutq_moe_mlp(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* gate_up,
+                 const lutq_mx_packed_t* down, const int32_t* ids, const float* weights,
+                 const int32_t* plan, int T, int k, void* workspace, size_t workspace_bytes,
+                 void* y, void* stream) {
+  int rc = check_packed(gate_up);
+  if (rc) return rc;
+  rc = check_packed(down);
+  if (rc) return rc;
+  if (!half_type(dtype)) return LUTQ_EINVAL;
+  const int E = gate_up->experts, D = gate_up->K, F = down->K;
+  if (down->experts != E || down->N != D || gate_up->N != 2LL * F) return LUTQ_EMISMATCH;
+  rc = check_route(T, E, k);
+  if (rc) return rc;
+  if (T == 0 || D == 0) return LUTQ_OK;
+  if (!y) return LUTQ_EINVAL;
+  if (!aligned(y, 8)) return LUTQ_EALIGN;
+  const hipStream_t s = (hipStream_t)stream;
+  if (F == 0) return status(launch_mx_zero(y, (long long)T * D, s));
+  if (!x || !ids || !weights || !plan || !workspace || ldx < D) return LUTQ_EINVAL;
+  if (!aligned(x, 16) || ldx % 8 || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(plan, 4) ||
+      !aligned(workspace, 16))
+    return LUTQ_EALIGN;
+  if (workspace_bytes < lutq_moe_workspace_bytes(T, k, D, F)) return LUTQ_ESIZE;
+  const long long pairs = (long long)T * k;
+  const MoePlanLayout l = moe_plan_layout(T, E, k);
+  if (!tiles_fit(l.max_tiles, 2LL * F) || !tiles_fit(l.max_tiles, D)) return LUTQ_EUNSUPPORTED;
+  const int cus = device_cu_count();
+  float* h = static_cast<float*>(workspace);
+  float* out = h + (size_t)pairs * F;  // F is a multiple of 32
+  MxParams up = {};
+  up.x = x;
+  up.ldx = ldx;
+  up.w = weights_of(gate_up);
+  up.y = h;
+  up.ids = ids;
+  up.weights = weights;
+  up.order = plan + l.order;
+  up.tiles = plan + l.tiles;
+  up.max_tiles = l.max_tiles;
+  up.pairs = (int)pairs;
+  up.topk = k;
+  up.experts = E;
+  MxParams dn = up;
+  dn.x = h;
+  dn.ldx = F;
+  dn.w = weights_of(down);
+  dn.M = T;
+  hipError_t e;
+  if (moe_direct(pairs, k, E)) {
+    e = launch_mx_stream(up, dtype, kMxUpPair, cus, s);
+    if (e != hipSuccess) return record_hip_error(e);
+    dn.y = y;
+    return status(launch_mx_stream(dn, dtype, kMxDownToken, cus, s));
+  }
+  dn.y = out;
+  const bool tiled = moe_tile_rows(pairs, E) > 16;
+  const auto product = tiled ? launch_mx_tile : launch_mx_stream;
+  e = product(up, dtype, kMxUp, cus, s);
+  if (e == hipSuccess) e = product(dn, dtype, kMxDown, cus, s);
+  if (e == hipSuccess) e = launch_moe_combine(out, ids, y, dtype, T, k, D, E, s);
+  return status(e);
+}
+
+}  // extern "C"

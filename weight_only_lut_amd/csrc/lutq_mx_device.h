@@ -1,0 +1,123 @@
+// Device building blocks of the MX4 products (gfx950 only).
+//
+// MFMA roles: the weights are the A operand (rows n), the activations the B
+// operand (columns m), so a lane ends with four consecutive n of one row of
+// y: D[n = 4q + i][m = r], lane = 16q + r. Within a 128-value chunk the K
+// order is free as long as both operands agree: step j multiplies, for lane
+// quarter q, values k = 32q + 8j .. + 7, so a lane's 16 bytes of codes are one
+// MX block with one scale.
+#pragma once
+
+#include "lutq_mx.h"
+
+namespace lutq {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// 16 zero bytes that loads past an edge are pointed at.
+static __device__ const u32x4 mx_zero16 = {0, 0, 0, 0};
+
+template <int DT> struct Mx16;
+
+// A decoded weight is code level * 2^(b - 127 + kShift), b the relative scale
+// byte (<= 127). fp16 has the fewer exponents: its largest block sits at
+// 6 * 2^13 < 65504, so blocks down to 2^-36 of it are exact; the row factor
+// takes the 2^13 back out.
+template <> struct Mx16<kF16> {
+  typedef f16x8 frag;
+  static constexpr int kType = kF16, kShift = 13;
+  static __device__ __forceinline__ frag decode(uint32_t w, float s) {
+    union { f16x2 h[4]; frag f; } o;
+    o.h[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0);
+    o.h[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1);
+    o.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2);
+    o.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3);
+    return o.f;
+  }
+  static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return __builtin_bit_cast(uint32_t, f16x2{(f16)a, (f16)b});
+  }
+};
+template <> struct Mx16<kBf16> {
+  typedef bf16x8 frag;
+  static constexpr int kType = kBf16, kShift = 0;
+  static __device__ __forceinline__ frag decode(uint32_t w, float s) {
+    union { bf16x2 h[4]; frag f; } o;
+    o.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+    o.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+    o.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+    o.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+    return o.f;
+  }
+  static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ float mx_scale(uint32_t b) {
+  return __builtin_bit_cast(float, (b << 23) + ((uint32_t)Mx16<DT>::kShift << 23));
+}
+
+// Eight fp32 values as a bf16 fragment plus the bf16 fragment of what that
+// leaves: 16 bits of significand over the whole range of fp32.
+__device__ __forceinline__ void split_bf16(const f32x4& a, const f32x4& b, bf16x8& hi, bf16x8& lo) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = i < 4 ? a[i] : b[i - 4];
+    const __bf16 h = (__bf16)v;
+    hi[i] = h;
+    lo[i] = (__bf16)(v - (float)h);
+  }
+}
+
+__device__ __forceinline__ f32x4 row_factors(const float* rows, int n, int shift) {
+  f32x4 v = *reinterpret_cast<const f32x4*>(rows + n);
+  const float back = shift ? 1.0f / 8192.0f : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] *= back;
+  return v;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g / (1.0f + __expf(-g)) * u;
+}
+
+// Four consecutive outputs n .. n + 3 of one row of width N, rounded to DT.
+template <int DT>
+__device__ __forceinline__ void store4(uint16_t* row, int n, int N, const f32x4& v) {
+  const uint32_t a = Mx16<DT>::pack(v[0], v[1]), b = Mx16<DT>::pack(v[2], v[3]);
+  if ((N & 3) == 0) {
+    if (n < N) *reinterpret_cast<u32x2*>(row + n) = u32x2{a, b};
+  } else {
+    if (n < N) row[n] = (uint16_t)a;
+    if (n + 1 < N) row[n + 1] = (uint16_t)(a >> 16);
+    if (n + 2 < N) row[n + 2] = (uint16_t)b;
+    if (n + 3 < N) row[n + 3] = (uint16_t)(b >> 16);
+  }
+}
+__device__ __forceinline__ void store4(float* row, int n, int N, const f32x4& v) {
+  if ((N & 3) == 0) {
+    if (n < N) *reinterpret_cast<f32x4*>(row + n) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) row[n + i] = v[i];
+  }
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; this numbering gives each XCD
+// a contiguous run of tiles, so that neighbours share its L2.
+__device__ __forceinline__ unsigned xcd_contiguous(unsigned id, unsigned total) {
+  const unsigned xcd = id & 7u, i = id >> 3, per = total >> 3, extra = total & 7u;
+  return xcd * per + (xcd < extra ? xcd : extra) + i;
+}
+
+}  // namespace lutq

@@ -1,0 +1,266 @@
+// Microscaled 4-bit floating point (gfx950): quantization, its inverse, and
+// the packing of weights for the products.
+//
+// Per block of 32 values along K: top = max |x|, the scale 2^e with
+// e = floor(log2 top) - 2 (2 is the exponent of the largest level, 6 = 1.5 *
+// 2^2) or, under the ceil rule, one more when top > 6 * 2^e; each value is
+// x / 2^e (exact) rounded to the nearest of {0, .5, 1, 1.5, 2, 3, 4, 6}, ties
+// to the even code, by gfx950's scaled conversion.
+//
+// Bound by memory: 8 values per lane, so that a block spans a quad and its
+// maximum takes two DPP steps, loads are 16 bytes and a wave's code stores
+// are one run of 256 bytes. Contiguous rows are one long row (K is whole
+// blocks), which leaves no ragged edge but the last.
+#include "lutq_mx.h"
+
+namespace lutq {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 256;
+constexpr int kLaneValues = 8;
+
+template <int DT>
+__device__ __forceinline__ f32x8 load8(const void* x, long long e) {
+  f32x8 v;
+  if constexpr (DT == kF32) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(x) + e);
+    const f32x4 a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+  } else {
+    const u32x4 d = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + e));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = d[i];
+      if constexpr (DT == kF16) {
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        v[2 * i] = (float)h[0];
+        v[2 * i + 1] = (float)h[1];
+      } else {
+        v[2 * i] = __builtin_bit_cast(float, w << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
+      }
+    }
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
+  v = v > o ? v : o;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
+
+// Codes and the scale byte of one lane's 8 values; the quad holds the block.
+__device__ __forceinline__ uint32_t quantize8(const f32x8& v, int rule, uint32_t& scale) {
+  uint32_t top = 0;  // bits of |x|: their integer order is the order of magnitude, NaN above all
+#pragma unroll
+  for (int i = 0; i < kLaneValues; ++i) {
+    const float f = v[i];  // (a bit cast of the vector element itself reads element 0)
+    const uint32_t a = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
+    top = top > a ? top : a;
+  }
+  top = quad_max(top);
+  int e = (int)(top >> 23) - 2;  // a subnormal top clamps to 2^-127 either way
+  if (rule != 0 && (top & 0x7FFFFFu) > 0x400000u) ++e;
+  e = e < 0 ? 0 : e;
+  const bool bad = top >= 0x7F800000u;
+  // 2^(e - 127); e = 0 is the subnormal 2^-127
+  const float s = __builtin_bit_cast(float, e > 0 ? (uint32_t)e << 23 : 0x00400000u);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+  scale = bad ? 255u : (uint32_t)e;
+  return bad ? 0u : c;
+}
+
+// UNITS units of 8 values per thread, a block's width apart so that each
+// load and store of the workgroup is contiguous; all loads are issued first.
+template <int DT, int UNITS>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void* x, long long row_values,
+                                                                long long ldx, int rule,
+                                                                uint8_t* codes, uint8_t* scales) {
+  const long long row = blockIdx.y;
+  const long long base = ((long long)blockIdx.x * UNITS * kThreads + threadIdx.x) * kLaneValues;
+  f32x8 v[UNITS];
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const long long at = base + (long long)u * kThreads * kLaneValues;
+    if (at < row_values) v[u] = load8<DT>(x, row * ldx + at);
+  }
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const long long at = base + (long long)u * kThreads * kLaneValues;
+    if (at < row_values) {  // whole quads: row_values is a multiple of 32
+      uint32_t scale;
+      const uint32_t c = quantize8(v[u], rule, scale);
+      const long long out = row * row_values + at;
+      *reinterpret_cast<uint32_t*>(codes + out / 2) = c;
+      if ((threadIdx.x & 3) == 0) scales[out / kMxBlock] = (uint8_t)scale;
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* codes,
+                                                                  const uint8_t* scales,
+                                                                  long long values, void* x) {
+  const long long step = (long long)gridDim.x * kThreads * kLaneValues;
+  for (long long at = ((long long)blockIdx.x * kThreads + threadIdx.x) * kLaneValues; at < values;
+       at += step) {
+    const uint32_t c = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes + at / 2));
+    const uint32_t b = scales[at / kMxBlock];
+    const float s = __builtin_bit_cast(float, b == 0 ? 0x00400000u : b << 23);
+    f32x8 v;
+#define LUTQ_PAIR(i)                                                              \
+  {                                                                               \
+    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, i);             \
+    v[2 * i] = p[0];                                                              \
+    v[2 * i + 1] = p[1];                                                          \
+  }
+    LUTQ_PAIR(0) LUTQ_PAIR(1) LUTQ_PAIR(2) LUTQ_PAIR(3)
+#undef LUTQ_PAIR
+    if constexpr (DT == kF32) {
+      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(x) + at);
+      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, o);
+      __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, o + 1);
+    } else {
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == kF16) {
+          o[i] = __builtin_bit_cast(uint32_t, f16x2{(f16)v[2 * i], (f16)v[2 * i + 1]});
+        } else {
+          o[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+        }
+      }
+      __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(x) + at));
+    }
+  }
+}
+
+// One workgroup per tile of 16 rows: the rows' largest scales over blocks
+// that hold a nonzero code, then the codes and relative scales moved to their
+// slots, 16 bytes and 1 byte per lane.
+__global__ __launch_bounds__(kThreads) void mx_pack_kernel(const uint8_t* codes,
+                                                            const uint8_t* scales, int N, int K,
+                                                            MxLayout l, uint8_t* out_codes,
+                                                            uint8_t* out_scales, float* out_rows) {
+  __shared__ int top[kTileRows];  // largest scale byte, or 256 once a block is NaN
+  const int t = blockIdx.x;
+  const size_t expert = blockIdx.y;
+  const int r = threadIdx.x % kTileRows, part = threadIdx.x / kTileRows;
+  const int n = t * kTileRows + r;
+  const int kb = K / kMxBlock;
+  const size_t row = expert * N + n;
+  const u32x4* c16 = reinterpret_cast<const u32x4*>(codes + row * (size_t)(K / 2));
+  const uint8_t* s8 = scales + row * (size_t)kb;
+  if (threadIdx.x < kTileRows) top[threadIdx.x] = 0;
+  __syncthreads();
+  if (n < N) {
+    int m = 0;
+    for (int b = part; b < kb; b += kThreads / kTileRows) {
+      const u32x4 c = c16[b];
+      const int s = s8[b];
+      if (s == 255) m = 256;
+      else if (((c.x | c.y | c.z | c.w) & 0x77777777u) && s > m) m = s;
+    }
+    if (m) atomicMax(&top[r], m);
+  }
+  __syncthreads();
+  const bool nan = top[r] == 256;
+  const int ref = nan ? 0 : top[r];
+  out_codes += expert * l.code_bytes + (size_t)t * l.nchunk * kMxBlockBytes;
+  out_scales += expert * l.scale_bytes + (size_t)t * l.nquad * kWave * 4;
+  // slot 16q + r of chunk c is block 4c + q of row r: thread `part` takes
+  // blocks part, part + 16, ...
+  for (int b = part; b < l.nquad * 16; b += kThreads / kTileRows) {
+    const int c = b / 4, q = b % 4;
+    const bool in = n < N && b < kb && !nan;
+    if (c < l.nchunk)
+      *reinterpret_cast<u32x4*>(out_codes + (size_t)c * kMxBlockBytes + (q * 16 + r) * kMxSlotBytes) =
+          in ? c16[b] : u32x4{0, 0, 0, 0};
+    int rel = 0;
+    if (in) {
+      // an all-zero block may carry a scale above the row's largest
+      const int s = s8[b];
+      rel = s > ref ? 127 : s - ref + 127;
+      rel = rel < 0 ? 0 : rel;
+    }
+    out_scales[((size_t)(c / 4) * kWave + q * 16 + r) * 4 + c % 4] = (uint8_t)rel;
+  }
+  if (part == 0)
+    out_rows[expert * (l.row_bytes / sizeof(float)) + n] =
+        nan ? __builtin_nanf("") : n < N ? __builtin_ldexpf(1.0f, ref - 127) : 0.0f;
+}
+
+template <int DT>
+hipError_t quantize(const void* x, int rows, long long row_values, long long ldx, int rule,
+                    uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  const long long wide = 4LL * kThreads * kLaneValues, narrow = (long long)kThreads * kLaneValues;
+  // four units per thread keep enough loads in flight to stream; a call of
+  // few workgroups spreads wider instead
+  const bool few = (row_values + wide - 1) / wide * rows < 1024;
+  const long long per = few ? narrow : wide;
+  const unsigned gx = (unsigned)((row_values + per - 1) / per);
+  for (long long r0 = 0; r0 < rows; r0 += 65535) {  // grid.y
+    const unsigned gy = (unsigned)(rows - r0 < 65535 ? rows - r0 : 65535);
+    const char* xr = static_cast<const char*>(x) + r0 * ldx * (DT == kF32 ? 4 : 2);
+    uint8_t* cr = codes + r0 * row_values / 2;
+    uint8_t* sr = scales + r0 * row_values / kMxBlock;
+    if (few) mx_quantize_kernel<DT, 1><<<dim3(gx, gy), kThreads, 0, s>>>(xr, row_values, ldx, rule, cr, sr);
+    else mx_quantize_kernel<DT, 4><<<dim3(gx, gy), kThreads, 0, s>>>(xr, row_values, ldx, rule, cr, sr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void* x, int dtype, int rows, int K, long long ldx, int rule,
+                              uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  long long row_values = K;
+  if (ldx == K) {  // contiguous: one long row
+    row_values *= rows;
+    rows = 1;
+  }
+  switch (dtype) {
+    case kF32: return quantize<kF32>(x, rows, row_values, ldx, rule, codes, scales, s);
+    case kF16: return quantize<kF16>(x, rows, row_values, ldx, rule, codes, scales, s);
+    default: return quantize<kBf16>(x, rows, row_values, ldx, rule, codes, scales, s);
+  }
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype,
+                                long long values, void* x, hipStream_t s) {
+  const long long per = (long long)kThreads * kLaneValues;
+  long long blocks = (values + per - 1) / per;
+  if (blocks > 1 << 20) blocks = 1 << 20;
+  const dim3 g((unsigned)blocks);
+  switch (dtype) {
+    case kF32: mx_dequantize_kernel<kF32><<<g, kThreads, 0, s>>>(codes, scales, values, x); break;
+    case kF16: mx_dequantize_kernel<kF16><<<g, kThreads, 0, s>>>(codes, scales, values, x); break;
+    default: mx_dequantize_kernel<kBf16><<<g, kThreads, 0, s>>>(codes, scales, values, x);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N, int K,
+                          void* dst, hipStream_t s) {
+  const MxLayout l = mx_layout(N, K);
+  uint8_t* c = static_cast<uint8_t*>(dst);
+  uint8_t* sc = c + l.code_bytes * experts;
+  float* rows = reinterpret_cast<float*>(sc + l.scale_bytes * experts);
+  mx_pack_kernel<<<dim3(l.ntile, experts), kThreads, 0, s>>>(codes, scales, N, K, l, c, sc, rows);
+  return hipGetLastError();
+}
+
+}  // namespace lutq
