@@ -45,7 +45,7 @@ def quantize(x, rule="floor"):
 
 def dequantize(codes, scales):
     """fp64 values [..., K]."""
-    n = np.stack((codes & 15, codes >> 4), -1).reshape(*codes.shape[:-1], -1)
+    n = np.stack((codes & 15, codes >> 4), -1).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
     v = LEVELS[n & 7] * np.where(n & 8, -1.0, 1.0)
     s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(int) - 127))
     return v * np.repeat(s, BLOCK, -1)

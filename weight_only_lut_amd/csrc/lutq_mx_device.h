@@ -18,6 +18,19 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // 16 zero bytes that loads past an edge are pointed at.
 static __device__ const u32x4 mx_zero16 = {0, 0, 0, 0};
 
+// 16 bytes per lane from memory into LDS at `dst` + 16 * lane, without passing
+// through registers; complete at the next barrier. `dst` is uniform.
+__device__ __forceinline__ void load_to_lds(const void* src, void* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// The same through a buffer resource: zeros come from offsets past its end.
+__device__ __forceinline__ void buffer_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t offset, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, offset,
+                                           0, 0, 0);
+}
+
 template <int DT> struct Mx16;
 
 // A decoded weight is code level * 2^(b - 127 + kShift), b the relative scale

@@ -22,7 +22,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxParams p, int m
   constexpr int kThreads = WM * WN * 64;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr int kLoads = BM * 16 / kThreads;  // 16-byte pieces per thread and chunk
-  __shared__ u32x4 xs[2][BM * 16];
+  __shared__ u32x4 xs0[BM * 16], xs1[BM * 16];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
@@ -48,17 +48,29 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxParams p, int m
   }
   const MxWeights& w = p.w;
 
-  // this thread's pieces: row and (swizzled) column of piece i * kThreads + tid
-  const uint16_t* xp[kLoads];
-  const int slot = threadIdx.x & 15;
-  int col[kLoads];
+  // This thread's pieces of the activations' tile: piece i is row
+  // i * kRowStep + tid / 16, column slot ^ (row & 15), the same for every i.
+  constexpr int kRowStep = kThreads / 16;
+  static_assert(kRowStep % 16 == 0, "a thread's pieces share their column");
+  const int prow = threadIdx.x >> 4;
+  const int col = ((threadIdx.x & 15) ^ (prow & 15)) * 8;
+  // Rows in order go through a buffer resource, whose end makes rows past the
+  // last read as zeros; gathered rows take a pointer each.
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t at = 0, row_step = 0;
+  const uint16_t* xp[kUp ? kLoads : 1];
+  if constexpr (kUp) {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int row = (i * kThreads + (int)threadIdx.x) >> 4;
-    long long src = row0 + (row < rows ? row : rows - 1);  // rows past the end are computed, not stored
-    if constexpr (kUp) src = p.order[src] / p.topk;
-    col[i] = (slot ^ (row & 15)) * 8;
-    xp[i] = static_cast<const uint16_t*>(p.x) + src * p.ldx + col[i];
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = i * kRowStep + prow;
+      const long long src = p.order[row0 + (row < rows ? row : rows - 1)] / p.topk;
+      xp[i] = static_cast<const uint16_t*>(p.x) + src * p.ldx + col;
+    }
+  } else {
+    rs = make_rsrc(static_cast<const uint16_t*>(p.x) + row0 * p.ldx,
+                   (uint32_t)(((rows - 1) * p.ldx + w.K) * 2));
+    at = (uint32_t)((prow * p.ldx + col) * 2);
+    row_step = (uint32_t)(kRowStep * p.ldx * 2);
   }
   const uint8_t* codes = w.codes + expert * w.expert_codes;
   const uint8_t* scales = w.scales + expert * w.expert_scales;
@@ -80,16 +92,17 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxParams p, int m
 #pragma unroll
     for (int m = 0; m < MI; ++m) acc[i][m] = f32x4{0, 0, 0, 0};
 
-  u32x4 xr[kLoads];
-  auto load_x = [&](int c) {
+  // Chunk c of the activations, straight into LDS; the last chunk may end
+  // inside, where zeros come in its place.
+  auto load_x = [&](int c, u32x4* stage) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const u32x4* src = reinterpret_cast<const u32x4*>(xp[i] + (size_t)c * kChunk);
-      xr[i] = *(c * kChunk + col[i] < w.K ? src : &mx_zero16);
+      u32x4* dst = stage + i * kThreads + wave * kWave;
+      const bool past = (c + 1) * kChunk > w.K && c * kChunk + col >= w.K;
+      if constexpr (kUp) load_to_lds(past ? static_cast<const void*>(&mx_zero16) : xp[i] + (size_t)c * kChunk, dst);
+      else buffer_to_lds(rs, past ? kOutOfRange : at + i * row_step + c * (kChunk * 2), dst);
     }
   };
-  u32x4 cd[2][NI];
-  uint32_t sc[2][NI];
   auto load_w = [&](int c, u32x4* d, uint32_t* s) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -98,42 +111,41 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxParams p, int m
       s[i] = scales[((size_t)tile[i] * w.nquad + c / 4) * (kWave * 4) + lane * 4 + c % 4];
     }
   };
-  auto store_x = [&](int stage) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) xs[stage][i * kThreads + threadIdx.x] = xr[i];
-  };
-  load_x(0);
-  load_w(0, cd[0], sc[0]);
-  store_x(0);
   const int base = (wm * MI * 16 + r) * 16;
-  auto step = [&](int c, int stage) {
+  // One chunk: the next one's loads go out first. The barrier also waits for
+  // this chunk's activations, and for every wave to be done with the other
+  // stage.
+  auto step = [&](int c, const u32x4* cur, u32x4* next, const u32x4* d, const uint32_t* s, u32x4* dn,
+                  uint32_t* sn) {
     __syncthreads();
-    const bool more = c + 1 < w.nchunk;
-    if (more) {
-      load_x(c + 1);
-      load_w(c + 1, cd[stage ^ 1], sc[stage ^ 1]);
+    if (c + 1 < w.nchunk) {
+      load_x(c + 1, next);
+      load_w(c + 1, dn, sn);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       frag b[MI];
 #pragma unroll
       for (int m = 0; m < MI; ++m)
-        b[m] = __builtin_bit_cast(frag, xs[stage][base + m * 256 + ((4 * q + j) ^ r)]);
+        b[m] = __builtin_bit_cast(frag, cur[base + m * 256 + ((4 * q + j) ^ r)]);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const frag a = T::decode(cd[stage][i][j], mx_scale<DT>(sc[stage][i]));
+        const frag a = T::decode(d[i][j], mx_scale<DT>(s[i]));
 #pragma unroll
         for (int m = 0; m < MI; ++m) acc[i][m] = T::mfma(a, b[m], acc[i][m]);
       }
     }
-    if (more) store_x(stage ^ 1);
   };
+  u32x4 d0[NI], d1[NI];
+  uint32_t s0[NI], s1[NI];
+  load_x(0, xs0);
+  load_w(0, d0, s0);
   int c = 0;
   for (; c + 1 < w.nchunk; c += 2) {
-    step(c, 0);
-    step(c + 1, 1);
+    step(c, xs0, xs1, d0, s0, d1, s1);
+    step(c + 1, xs1, xs0, d1, s1, d0, s0);
   }
-  if (c < w.nchunk) step(c, 0);
+  if (c < w.nchunk) step(c, xs0, xs1, d0, s0, d1, s1);
 
   constexpr int kOut = kUp ? NI / 2 : NI;
   const int N = kUp ? half * 16 : w.N;
