@@ -98,7 +98,8 @@ int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N
 /* ---- products ------------------------------------------------------------------
  * y[m, n] = sum_k x[m, k] * w[n, k], one matrix (experts == 1).
  *   x      : device, fp16 or bf16 (`dtype`) [M][K], row stride ldx elements,
- *            16-byte aligned, ldx >= K and a multiple of 8.
+ *            16-byte aligned, ldx >= K, a multiple of 8 and at most 2^22
+ *            (LUTQ_EUNSUPPORTED).
  *   y      : device, [M][N] contiguous in `dtype`, 8-byte aligned.
  * fp32 accumulation on the matrix cores; y is rounded once, to nearest even.
  * The weights enter exactly, with their row's largest scale taken out and
@@ -115,14 +116,22 @@ enum {
   LUTQ_MX_PATH_TILE = 2    /* tiles of 64-256 rows through on-chip memory           */
 };
 int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,
-                   int M, int N, int K, int path, void* stream);
+                   int M, int N, int K, int path, void* workspace, size_t workspace_bytes,
+                   void* stream);
 
 /* The same with 4-bit activations: xcodes [M][K/2] and xscales [M][K/32] as
  * lutq_mx_quantize writes them, both operands in 4 bits on the scaled matrix
  * instructions; `dtype` (fp16 or bf16) is y's.
  *   xcodes : 16-byte aligned. */
 int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
-                      void* y, int dtype, int M, int N, int K, void* stream);
+                      void* y, int dtype, int M, int N, int K, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the two products need (device, caller-owned, 16-byte
+ * aligned, free for other use once the call's work is done; may be NULL where
+ * this is 0; LUTQ_ESIZE if it is smaller). four_bit: 1 for lutq_mx_matmul_mx.
+ * 0 for invalid sizes. */
+size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit);
 
 #ifdef __cplusplus
 }

@@ -69,22 +69,27 @@ def test_pack_refuses(lib):
 def test_matmul_refuses(lib):
     def m(x=P, dtype=2, ldx=64, desc=None, y=P, M=2, N=48, K=64, path=0, **over):
         d = desc or _desc(**over)
-        return lib.lutq_mx_matmul(x, dtype, ldx, ctypes.addressof(d), y, M, N, K, path, None)
+        return lib.lutq_mx_matmul(x, dtype, ldx, ctypes.addressof(d), y, M, N, K, path, None, 0, None)
     assert m(M=0) == OK
     assert m(x=None) == m(y=None) == m(dtype=0) == m(path=3) == m(M=-1) == m(ldx=63) == EINVAL
     assert m(N=47) == m(K=32) == m(magic=0) == m(version=2) == m(nbytes=16) == EMISMATCH
     assert m(desc=_desc(E=2)) == EMISMATCH
     assert m(data=None) == EINVAL
     assert m(x=P + 2) == m(y=P + 4) == m(ldx=66) == m(data=P + 8) == EALIGN
-    assert lib.lutq_mx_matmul(P, 2, 64, None, P, 1, 48, 64, 0, None) == EINVAL
+    assert lib.lutq_mx_matmul(P, 2, 64, None, P, 1, 48, 64, 0, None, 0, None) == EINVAL
+    assert m(ldx=(1 << 22) + 8) == EUNSUP
 
-    def m4(xc=P, xs=P, y=P, dtype=2, M=2, N=48, K=64, **over):
+    need = lib.lutq_mx_workspace_bytes(2, 48, 64, 1)
+    assert need > 0 and lib.lutq_mx_workspace_bytes(0, 48, 64, 1) == 0 == lib.lutq_mx_workspace_bytes(2, 48, 63, 1)
+
+    def m4(xc=P, xs=P, y=P, dtype=2, M=2, N=48, K=64, ws=P, n=need, **over):
         d = _desc(**over)
-        return lib.lutq_mx_matmul_mx(xc, xs, ctypes.addressof(d), y, dtype, M, N, K, None)
+        return lib.lutq_mx_matmul_mx(xc, xs, ctypes.addressof(d), y, dtype, M, N, K, ws, n, None)
     assert m4(M=0) == OK
     assert m4(xc=None) == m4(xs=None) == m4(y=None) == m4(dtype=0) == m4(M=-2) == EINVAL
     assert m4(N=16) == m4(K=96) == EMISMATCH
-    assert m4(xc=P + 8) == m4(y=P + 2) == EALIGN
+    assert m4(xc=P + 8) == m4(y=P + 2) == m4(ws=P + 8) == EALIGN
+    assert m4(ws=None) == EINVAL and m4(n=need - 1) == ESIZE
 
 
 def _opts(**over):

@@ -30,7 +30,7 @@ EXPORTS = (
     "lutq_peak_lds",
     # include/lutq_mx.h
     "lutq_mx_quantize", "lutq_mx_dequantize", "lutq_mx_packed_bytes", "lutq_mx_pack",
-    "lutq_mx_matmul", "lutq_mx_matmul_mx",
+    "lutq_mx_matmul", "lutq_mx_matmul_mx", "lutq_mx_workspace_bytes",
     # include/lutq_moe.h
     "lutq_moe_route", "lutq_moe_plan_ints", "lutq_moe_plan", "lutq_moe_workspace_bytes",
     "lutq_moe_mlp",

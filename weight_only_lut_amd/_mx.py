@@ -47,8 +47,9 @@ def declare(lib):
             ("lutq_mx_dequantize", i32, [vp, vp, i32, i32, i32, vp, vp]),
             ("lutq_mx_packed_bytes", sz, [i32, i32, i32]),
             ("lutq_mx_pack", i32, [vp, vp, i32, i32, i32, vp, sz, vp, vp]),
-            ("lutq_mx_matmul", i32, [vp, i32, i64, vp, vp, i32, i32, i32, i32, vp]),
-            ("lutq_mx_matmul_mx", i32, [vp, vp, vp, vp, i32, i32, i32, i32, vp]),
+            ("lutq_mx_matmul", i32, [vp, i32, i64, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
+            ("lutq_mx_matmul_mx", i32, [vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
+            ("lutq_mx_workspace_bytes", sz, [i32, i32, i32, i32]),
             ("lutq_moe_route", i32, [vp, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp]),
             ("lutq_moe_plan_ints", sz, [i32, i32, i32]),
             ("lutq_moe_plan", i32, [vp, i32, i32, i32, vp, vp]),
@@ -202,12 +203,15 @@ def mx_matmul(x, p: MxPacked, *, dtype=None, path: str = "auto", out=None):
         dev = x.device
     if out is None:
         out = torch.empty((M, p.N), dtype=dtype, device=dev)
+    lib = _lib()
+    nbytes = lib.lutq_mx_workspace_bytes(M, p.N, K, four)
+    space = torch.empty(nbytes, dtype=torch.uint8, device=dev).data_ptr() if nbytes else None
     if four:
-        rc = _lib().lutq_mx_matmul_mx(xc.data_ptr(), xs.data_ptr(), p._ref, out.data_ptr(), _HALF[dtype], M,
-                                      p.N, K, _raw_stream(dev))
+        rc = lib.lutq_mx_matmul_mx(xc.data_ptr(), xs.data_ptr(), p._ref, out.data_ptr(), _HALF[dtype], M,
+                                   p.N, K, space, nbytes, _raw_stream(dev))
     else:
-        rc = _lib().lutq_mx_matmul(x.data_ptr(), _HALF[dtype], ldx, p._ref, out.data_ptr(), M, p.N, K,
-                                   _PATHS[path], _raw_stream(dev))
+        rc = lib.lutq_mx_matmul(x.data_ptr(), _HALF[dtype], ldx, p._ref, out.data_ptr(), M, p.N, K,
+                                _PATHS[path], space, nbytes, _raw_stream(dev))
     if rc:
         raise LutqError(rc, "lutq_mx_matmul")
     return out

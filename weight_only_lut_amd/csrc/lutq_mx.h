@@ -60,8 +60,9 @@ struct MxParams {
   const uint8_t* xscales;
   long long ldx;         // elements (bytes for 4-bit codes)
   MxWeights w;
-  void* y;               // dense: 16-bit [M][N]; up: h [pairs][F], fp32 (stream) or 16-bit
-                         // (tile); down: fp32 [pairs][D]; down-token: 16-bit [T][D]
+  void* y;               // dense: 16-bit [M][N]; up: h [pairs][F], two bf16 planes (stream) or
+                         // 16-bit (tile); down: fp32 [pairs][D]; down-token: 16-bit [T][D]
+  long long plane;       // elements between the planes of h
   int M;                 // dense: rows
   // grouped
   const int32_t* ids;
@@ -70,7 +71,13 @@ struct MxParams {
   const int32_t* tiles;  // [0] the count, then {expert, first position, rows, 0} from [4]
   int max_tiles;         // entries at most (the grid)
   int pairs, topk, experts;
+  void* workspace;       // the caller's, as the launcher needs it
 };
+
+// Bytes of M rows' scales in the tile order of packed weights.
+inline size_t mx_scale_tile_bytes(long long M, int K) {
+  return (size_t)((M + 15) / 16) * ((K + 4 * kChunk - 1) / (4 * kChunk)) * kWave * 4;
+}
 
 // Rows of a grouped row tile, by the average number of pairs per expert:
 // what the plan cuts and the product kernels are compiled for.

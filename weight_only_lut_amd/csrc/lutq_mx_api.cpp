@@ -75,6 +75,16 @@ int check_route(int T, int E, int k) {
   return LUTQ_OK;
 }
 
+// Elements of a row stride at most: a tile's rows are addressed with 32 bits.
+constexpr long long kMaxLd = 1 << 22;
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (!need) return LUTQ_OK;
+  if (!ws) return LUTQ_EINVAL;
+  if (!aligned(ws, 16)) return LUTQ_EALIGN;
+  return have < need ? LUTQ_ESIZE : LUTQ_OK;
+}
+
 // Whether a launch over row tiles x column tiles of at least 64 fits a grid.
 bool tiles_fit(long long row_tiles, long long N) { return row_tiles * ((N + 63) / 64) <= 0x7FFFFFFF; }
 
@@ -155,8 +165,14 @@ int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N
   return LUTQ_OK;
 }
 
+size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit) {
+  if (M <= 0 || check_weights(1, N, K) || N == 0 || K == 0) return 0;
+  return four_bit ? mx_scale_tile_bytes(M, K) : 0;
+}
+
 int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,
-                   int M, int N, int K, int path, void* stream) {
+                   int M, int N, int K, int path, void* workspace, size_t workspace_bytes,
+                   void* stream) {
   int rc = check_packed(packed);
   if (rc) return rc;
   if (M < 0 || N < 0 || K < 0 || !half_type(dtype) || path < LUTQ_MX_PATH_AUTO ||
@@ -171,7 +187,11 @@ int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed
   if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
   if (!x || ldx < K) return LUTQ_EINVAL;
   if (!aligned(x, 16) || ldx % 8) return LUTQ_EALIGN;
+  if (ldx > kMaxLd) return LUTQ_EUNSUPPORTED;
+  rc = check_workspace(workspace, workspace_bytes, lutq_mx_workspace_bytes(M, N, K, 0));
+  if (rc) return rc;
   MxParams p = {};
+  p.workspace = workspace;
   p.x = x;
   p.ldx = ldx;
   p.w = weights_of(packed);
@@ -183,7 +203,8 @@ int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed
 }
 
 int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
-                      void* y, int dtype, int M, int N, int K, void* stream) {
+                      void* y, int dtype, int M, int N, int K, void* workspace,
+                      size_t workspace_bytes, void* stream) {
   int rc = check_packed(packed);
   if (rc) return rc;
   if (M < 0 || N < 0 || K < 0 || !half_type(dtype)) return LUTQ_EINVAL;
@@ -196,7 +217,10 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
   if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
   if (!xcodes || !xscales) return LUTQ_EINVAL;
   if (!aligned(xcodes, 16)) return LUTQ_EALIGN;
+  rc = check_workspace(workspace, workspace_bytes, lutq_mx_workspace_bytes(M, N, K, 1));
+  if (rc) return rc;
   MxParams p = {};
+  p.workspace = workspace;
   p.x = xcodes;
   p.xscales = xscales;
   p.ldx = K / 2;
@@ -259,7 +283,7 @@ int lutq_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, void* 
   return status(launch_moe_plan(ids, T, E, k, plan, (hipStream_t)stream));
 }
 
-// The workspace: h [pairs][F], sized for fp32, then fp32 [pairs][D] of the
+// The workspace: h [pairs][F], two bf16 planes at most, then fp32 [pairs][D] of the
 // pairs' outputs (not used where one workgroup sums a token's experts itself).
 size_t lutq_moe_workspace_bytes(int T, int k, int D, int F) {
   if (T < 0 || k < 1 || k > LUTQ_MOE_MAX_TOPK || D < 0 || F < 0) return 0;
@@ -289,6 +313,7 @@ int lutq_moe_mlp(const void* x, int dtype, long long ldx, const lutq_mx_packed_t
   if (!aligned(x, 16) || ldx % 8 || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(plan, 4) ||
       !aligned(workspace, 16))
     return LUTQ_EALIGN;
+  if (ldx > kMaxLd) return LUTQ_EUNSUPPORTED;
   if (workspace_bytes < lutq_moe_workspace_bytes(T, k, D, F)) return LUTQ_ESIZE;
   const long long pairs = (long long)T * k;
   const MoePlanLayout l = moe_plan_layout(T, E, k);
@@ -309,6 +334,7 @@ int lutq_moe_mlp(const void* x, int dtype, long long ldx, const lutq_mx_packed_t
   up.pairs = (int)pairs;
   up.topk = k;
   up.experts = E;
+  up.plane = pairs * F;
   MxParams dn = up;
   dn.x = h;
   dn.ldx = F;

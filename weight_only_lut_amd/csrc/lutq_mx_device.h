@@ -26,9 +26,11 @@ __device__ __forceinline__ void load_to_lds(const void* src, void* dst) {
 }
 
 // The same through a buffer resource: zeros come from offsets past its end.
-__device__ __forceinline__ void buffer_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t offset, void* dst) {
+// `base` is uniform and not part of the range check that matters here.
+__device__ __forceinline__ void buffer_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t offset, void* dst,
+                                              uint32_t base = 0) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, offset,
-                                           0, 0, 0);
+                                           base, 0, 0);
 }
 
 template <int DT> struct Mx16;
@@ -79,17 +81,39 @@ __device__ __forceinline__ float mx_scale(uint32_t b) {
   return __builtin_bit_cast(float, (b << 23) + ((uint32_t)Mx16<DT>::kShift << 23));
 }
 
-// Eight fp32 values as a bf16 fragment plus the bf16 fragment of what that
-// leaves: 16 bits of significand over the whole range of fp32.
-__device__ __forceinline__ void split_bf16(const f32x4& a, const f32x4& b, bf16x8& hi, bf16x8& lo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = i < 4 ? a[i] : b[i - 4];
-    const __bf16 h = (__bf16)v;
-    hi[i] = h;
-    lo[i] = (__bf16)(v - (float)h);
-  }
+// A 16-byte load known to be from global memory (a pointer chosen at run time
+// otherwise becomes a generic access, which also counts as an LDS access).
+__device__ __forceinline__ u32x4 global16(const void* p) {
+  return *(const __attribute__((address_space(1))) u32x4*)p;
 }
+__device__ __forceinline__ u32x4 buffer16(__amdgpu_buffer_rsrc_t rs, uint32_t offset) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, offset, 0, 0));
+}
+
+// One tile of packed weights as buffers: offsets past the tile's last chunk,
+// and every offset of an absent tile, read as zeros without a memory access.
+struct TileBuffers {
+  __amdgpu_buffer_rsrc_t codes, scales;
+};
+__device__ __forceinline__ TileBuffers tile_buffers(const MxWeights& w, size_t expert, int tile,
+                                                    bool present) {
+  TileBuffers b;
+  b.codes = make_rsrc(w.codes + expert * w.expert_codes + (size_t)tile * w.nchunk * kMxBlockBytes,
+                      present ? (uint32_t)w.nchunk * kMxBlockBytes : 0);
+  b.scales = make_rsrc(w.scales + expert * w.expert_scales + (size_t)tile * w.nquad * (kWave * 4),
+                       present ? (uint32_t)w.nquad * (kWave * 4) : 0);
+  return b;
+}
+// A lane's codes and scale byte of chunk c, streamed (read once).
+__device__ __forceinline__ u32x4 tile_codes(const TileBuffers& b, uint32_t c, int lane) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       b.codes, c * kMxBlockBytes + lane * kMxSlotBytes, 0, kNontemporal));
+}
+__device__ __forceinline__ uint32_t tile_scale(const TileBuffers& b, uint32_t c, int lane) {
+  return __builtin_amdgcn_raw_buffer_load_b8(b.scales, (c >> 2) * (kWave * 4) + lane * 4 + (c & 3), 0, 0);
+}
+// A chunk number past the end of every tile (K <= 2^20).
+constexpr uint32_t kNoChunk = 1u << 20;
 
 __device__ __forceinline__ f32x4 row_factors(const float* rows, int n, int shift) {
   f32x4 v = *reinterpret_cast<const f32x4*>(rows + n);

@@ -1,5 +1,5 @@
-// MX4 products for few rows: the packed weights stream once past 16 to 64
-// rows of activations (gfx950).
+// MX4 products for few rows: the packed weights stream once past 1 to 64 rows
+// of activations (gfx950).
 //
 // y[m][n] = rows[n] * sum_k x[m][k] * (level * relative scale)[n][k]. Bound by
 // the weights' bytes, 0.53 per value. A workgroup owns NT tiles of 16 weight
@@ -9,10 +9,16 @@
 // also at one row: 16 columns cost no more than one there, and the decode
 // (16 conversions per KiB and lane) is the same for either.
 //
-// The experts' modes keep h = silu(g) * u in fp32 (a few KB) and split it into
-// two bf16 fragments on the way into the down product, at no cost where bytes
-// bound it: of the operator's roundings only the last remains, and h has the
-// range of fp32 also in fp16 models.
+// Activations: a chunk of a row is 256 bytes that 16 neighbouring lanes read
+// together, and they reach the lanes that multiply them through a piece of
+// LDS of the wave's own. (Lanes reading their own operands, neighbours in
+// different rows, get 16 bytes per clock and CU: 30 us instead of 8 at 32
+// rows of 4096 x 14336.)
+//
+// The experts' modes keep h = silu(g) * u as two bf16 planes, the value and
+// what its rounding left, at no cost where bytes bound the products: of the
+// operator's roundings only the last remains, and h has the range of fp32
+// also in fp16 models.
 // Compiled once per activation type (LUTQ_MX_TYPE).
 #include <type_traits>
 
@@ -23,16 +29,35 @@ namespace {
 
 constexpr int DT = LUTQ_MX_TYPE;
 
+// Eight bf16 planes of h: 4 values n .. n + 3 of a row, hi and lo `plane` apart.
+__device__ __forceinline__ void store_h(uint16_t* row, size_t plane, const f32x4& v) {
+  f32x4 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    hi[e] = (float)(__bf16)v[e];
+    lo[e] = v[e] - hi[e];
+  }
+  *reinterpret_cast<u32x2*>(row) = u32x2{Mx16<kBf16>::pack(hi[0], hi[1]), Mx16<kBf16>::pack(hi[2], hi[3])};
+  *reinterpret_cast<u32x2*>(row + plane) =
+      u32x2{Mx16<kBf16>::pack(lo[0], lo[1]), Mx16<kBf16>::pack(lo[2], lo[3])};
+}
 
 // MODE (see MxMode): dense, up, down and up-pair. For the up modes half of
-// the NT tiles are gate rows and half the up rows that meet them.
-template <int MODE, int W, int NT, int MT, int U>
+// the NT tiles are gate rows and half the up rows that meet them. W waves;
+// RX loads of 4 rows cover the rows (16 * MT of them at most); U chunks are
+// in flight per wave.
+template <int MODE, int W, int NT, int RX, int U>
 __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
-  __shared__ f32x4 red[W][NT * MT][kWave];
   constexpr bool kUp = MODE == kMxUp || MODE == kMxUpPair;
   constexpr bool kDown = MODE == kMxDown;  // x is h
+  constexpr int MT = (RX + 3) / 4, PL = kDown ? 2 : 1;
   typedef Mx16<kDown ? kBf16 : DT> T;
   typedef typename T::frag frag;
+  // the waves' activations, then their sums
+  __shared__ union {
+    u32x4 x[W][PL][MT * 256];
+    f32x4 red[W][NT * MT][kWave];
+  } lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   int expert = 0, row0 = 0, rows = 0;
@@ -51,36 +76,41 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
     row0 = t[1];
     rows = t[2];
   }
-  typedef std::conditional_t<kDown, float, uint16_t> X;
-  constexpr int kVec = kDown ? 8 : 4;  // 16-byte loads of a lane's 32 values
-  const X* xp[MT];
-  bool live[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int m = mt * 16 + r;
-    live[mt] = m < rows;
-    long long src = row0 + (live[mt] ? m : 0);
-    if constexpr (MODE == kMxUp) src = p.order[src] / p.topk;
-    if constexpr (MODE == kMxUpPair) src = row0 / p.topk;
-    xp[mt] = static_cast<const X*>(p.x) + src * p.ldx + 32 * q;
-  }
   const MxWeights& w = p.w;
-  const uint8_t* codes = w.codes + expert * w.expert_codes;
-  const uint8_t* scales = w.scales + expert * w.expert_scales;
   const float* rowf = w.rows + expert * w.expert_rows;
-  int tile[NT];
+  // Load i of a chunk is rows 4i + q, 16 bytes per lane. Rows in order (dense,
+  // h) lie behind a buffer resource, gathered rows are pointers. Rows past
+  // the last read the last: their columns are not stored.
+  constexpr bool kGather = MODE == kMxUp;
+  __amdgpu_buffer_rsrc_t xrs[PL];
+  uint32_t xoff[RX];
+  const uint16_t* xp[kGather ? RX : 1];
+  {
+    const long long first = MODE == kMxUpPair ? row0 / p.topk : kGather ? 0 : row0;
+    const uint16_t* base = static_cast<const uint16_t*>(p.x) + first * p.ldx;
+    if constexpr (!kGather) {
+#pragma unroll
+      for (int z = 0; z < PL; ++z)
+        xrs[z] = make_rsrc(base + z * p.plane, (uint32_t)(((rows - 1) * p.ldx + w.K) * 2));
+    }
+#pragma unroll
+    for (int i = 0; i < RX; ++i) {
+      const int m = 4 * i + q, in = m < rows ? m : rows - 1;
+      if constexpr (kGather) xp[i] = base + (long long)(p.order[row0 + in] / p.topk) * p.ldx + 8 * r;
+      else xoff[i] = (uint32_t)((in * p.ldx + 8 * r) * 2);
+    }
+  }
+  TileBuffers tile[NT];
   const int half = w.ntile / 2;  // up modes: F / 16
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    int t;
     if constexpr (kUp) {
-      t = (int)blockIdx.x * (NT / 2) + i % (NT / 2);
-      t = (t < half ? t : half - 1) + (i < NT / 2 ? 0 : half);
+      const int t = (int)blockIdx.x * (NT / 2) + i % (NT / 2);
+      tile[i] = tile_buffers(w, expert, t + (i < NT / 2 ? 0 : half), t < half);
     } else {
-      t = (int)blockIdx.x * NT + i;
-      t = t < w.ntile ? t : w.ntile - 1;
+      const int t = (int)blockIdx.x * NT + i;
+      tile[i] = tile_buffers(w, expert, t, t < w.ntile);
     }
-    tile[i] = t;
   }
   f32x4 acc[NT][MT];
 #pragma unroll
@@ -91,57 +121,73 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   const int per = (w.nchunk + W - 1) / W;
   const int c0 = wave * per;
   const int c1 = c0 + per < w.nchunk ? c0 + per : w.nchunk;
-  for (int c = c0; c < c1; c += U) {
-    u32x4 cd[U][NT];
-    uint32_t sc[U][NT];
-    u32x4 xf[U][MT][kVec];
+  // U chunks in flight: each slot is refilled as soon as it is used. Loads
+  // past the wave's last chunk are out of range, so they touch no memory and
+  // every path has the same loads outstanding.
+  u32x4 cd[U][NT], xf[U][PL][RX];
+  uint32_t sc[U][NT];
+  auto load = [&](int u, int c) {
+    const bool in = c < c1;
+    const uint32_t cc = in ? (uint32_t)c : kNoChunk;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int cc = c + u < c1 ? c + u : c1 - 1;
+    for (int i = 0; i < NT; ++i) {
+      cd[u][i] = tile_codes(tile[i], cc, lane);
+      sc[u][i] = tile_scale(tile[i], cc, lane);
+    }
+    const bool valid = in && c * kChunk + 8 * r < w.K;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        cd[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-            codes + ((size_t)tile[i] * w.nchunk + cc) * kMxBlockBytes + lane * kMxSlotBytes));
-        sc[u][i] = scales[((size_t)tile[i] * w.nquad + cc / 4) * (kWave * 4) + lane * 4 + cc % 4];
-      }
+    for (int i = 0; i < RX; ++i) {
+      if constexpr (kGather) {
+        xf[u][0][i] = global16(valid ? static_cast<const void*>(xp[i] + (size_t)c * kChunk) : &mx_zero16);
+      } else {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const bool in = live[mt] && cc * kChunk + 32 * q < w.K;
-        const u32x4* src = reinterpret_cast<const u32x4*>(xp[mt] + (size_t)cc * kChunk);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) xf[u][mt][j] = in ? src[j] : u32x4{0, 0, 0, 0};
+        for (int z = 0; z < PL; ++z)
+          xf[u][z][i] = buffer16(xrs[z], valid ? xoff[i] + (uint32_t)c * (kChunk * 2) : kOutOfRange);
       }
     }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, c0 + u);
+  for (int c = c0; c < c1; c += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (c + u < c1) {
+      // piece s of row m sits at s ^ (m mod 16) of the row's sixteen: the 16
+      // rows that a fragment reads lie in different banks
+#pragma unroll
+      for (int z = 0; z < PL; ++z)
+#pragma unroll
+        for (int i = 0; i < RX; ++i)
+          lds.x[wave][z][(4 * i + q) * 16 + (r ^ ((4 * i + q) & 15))] = xf[u][z][i];
+      wave_lds_order();
+      float s[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s[i] = mx_scale<T::kType>(sc[u][i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        frag b[PL][MT];
+#pragma unroll
+        for (int z = 0; z < PL; ++z)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            b[z][mt] = __builtin_bit_cast(frag, lds.x[wave][z][(mt * 16 + r) * 16 + ((4 * q + j) ^ r)]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const float s = mx_scale<T::kType>(sc[u][i]);
+          const frag a = T::decode(cd[u][i][j], s[i]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const frag a = T::decode(cd[u][i][j], s);
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              if constexpr (kDown) {
-                frag hi, lo;
-                split_bf16(__builtin_bit_cast(f32x4, xf[u][mt][2 * j]),
-                           __builtin_bit_cast(f32x4, xf[u][mt][2 * j + 1]), hi, lo);
-                acc[i][mt] = T::mfma(a, lo, acc[i][mt]);
-                acc[i][mt] = T::mfma(a, hi, acc[i][mt]);
-              } else {
-                acc[i][mt] = T::mfma(a, __builtin_bit_cast(frag, xf[u][mt][j]), acc[i][mt]);
-              }
-            }
-          }
+            for (int z = PL - 1; z >= 0; --z) acc[i][mt] = T::mfma(a, b[z][mt], acc[i][mt]);
         }
       }
+      wave_lds_order();
+      load(u, c + u + U);
     }
   }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) red[wave][i * MT + mt][lane] = acc[i][mt];
+    for (int mt = 0; mt < MT; ++mt) lds.red[wave][i * MT + mt][lane] = acc[i][mt];
   __syncthreads();
 
   // a slot: four outputs n of one row m
@@ -150,22 +196,21 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
     const int l = s & 63, im = s >> 6, mt = im % MT, i = im / MT;
     const int m = mt * 16 + (l & 15);
     if (m >= rows) continue;
-    f32x4 v = red[0][im][l];
+    f32x4 v = lds.red[0][im][l];
 #pragma unroll
-    for (int k = 1; k < W; ++k) v += red[k][im][l];
+    for (int k = 1; k < W; ++k) v += lds.red[k][im][l];
     const int t = (int)blockIdx.x * kTiles + i;
     if (t >= (kUp ? half : w.ntile)) continue;
     const int n = t * 16 + 4 * (l >> 4);
     v *= row_factors(rowf, n, T::kShift);
     if constexpr (kUp) {
-      f32x4 u = red[0][im + kTiles * MT][l];
+      f32x4 u = lds.red[0][im + kTiles * MT][l];
 #pragma unroll
-      for (int k = 1; k < W; ++k) u += red[k][im + kTiles * MT][l];
+      for (int k = 1; k < W; ++k) u += lds.red[k][im + kTiles * MT][l];
       u *= row_factors(rowf, half * 16 + n, T::kShift);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], u[e]);
-      const int F = half * 16;
-      store4(static_cast<float*>(p.y) + (size_t)(row0 + m) * F, n, F, v);
+      store_h(static_cast<uint16_t*>(p.y) + (size_t)(row0 + m) * (half * 16) + n, p.plane, v);
     } else if constexpr (MODE == kMxDown) {
       const int pair = p.order[row0 + m];
       v *= p.weights[pair];
@@ -179,74 +224,80 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
 // The down products of one token's k <= 16 experts and their weighted sum in
 // one workgroup per NT tiles: pair j owns column j of the MFMAs, so one
 // accumulator holds all the experts' outputs apart, and the waves split the
-// k * nchunk blocks of weights between them.
+// k * nchunk blocks of weights between them. A block's 128 values of h are
+// 512 bytes of two planes, one load for half a wave.
 template <int W, int NT, int U>
 __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
+  typedef Mx16<kBf16> T;
+  typedef T::frag frag;
   __shared__ f32x4 red[W][NT][kWave];
+  __shared__ u32x4 hs[W][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int token = blockIdx.y, k = p.topk;
   const MxWeights& w = p.w;
   const int32_t* ids = p.ids + (size_t)token * k;
-  typedef Mx16<kBf16> T;
-  typedef T::frag frag;
-  const float* h = static_cast<const float*>(p.x) + (size_t)token * k * p.ldx + 32 * q;
-  int tile[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int t = (int)blockIdx.x * NT + i;
-    tile[i] = t < w.ntile ? t : w.ntile - 1;
-  }
+  // lanes 0-15: plane 0, lanes 16-31: plane 1, the rest out of range
+  const uint16_t* h = static_cast<const uint16_t*>(p.x) + (size_t)token * k * p.ldx;
+  const __amdgpu_buffer_rsrc_t hrs = make_rsrc(h, (uint32_t)((p.plane + k * p.ldx) * 2));
+  const uint32_t hoff = q < 2 ? (uint32_t)((q * p.plane + 8 * r) * 2) : kOutOfRange;
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
   const int units = k * w.nchunk, per = (units + W - 1) / W;
   const int u0 = wave * per;
   const int u1 = u0 + per < units ? u0 + per : units;
+  u32x4 cd[U][NT], xf[U];
+  uint32_t sc[U][NT];
+  int col[U];
+  auto load = [&](int u, int at) {
+    const bool in = at < u1;
+    const int j = in ? at / w.nchunk : 0, c = in ? at - j * w.nchunk : 0;
+    const int id = ids[j];
+    const bool valid = in && (unsigned)id < (unsigned)p.experts;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = (int)blockIdx.x * NT + i;
+      const TileBuffers b = tile_buffers(w, valid ? id : 0, t, valid && t < w.ntile);
+      cd[u][i] = tile_codes(b, c, lane);
+      sc[u][i] = tile_scale(b, c, lane);
+    }
+    // nothing was written to h of an absent pair
+    col[u] = valid ? j : 16;
+    xf[u] = buffer16(hrs, valid && c * kChunk + 8 * r < w.K
+                              ? hoff + (uint32_t)((j * p.ldx + c * kChunk) * 2)
+                              : kOutOfRange);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, u0 + u);
   for (int b = u0; b < u1; b += U) {
-    u32x4 cd[U][NT];
-    uint32_t sc[U][NT];
-    f32x4 xf[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = b + u < u1 ? b + u : u1 - 1;
-      const int j = at / w.nchunk, cc = at - j * w.nchunk;
-      const int id = ids[j];
-      const bool valid = (unsigned)id < (unsigned)p.experts;
-      const size_t e = valid ? id : 0;
+      if (lane < 32) hs[wave][lane] = xf[u];
+      wave_lds_order();
+      float s[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        cd[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-            w.codes + e * w.expert_codes + ((size_t)tile[i] * w.nchunk + cc) * kMxBlockBytes +
-            lane * kMxSlotBytes));
-        sc[u][i] = w.scales[e * w.expert_scales + ((size_t)tile[i] * w.nquad + cc / 4) * (kWave * 4) +
-                            lane * 4 + cc % 4];
-      }
-      // column j alone is not zero; nothing was written to h of an absent pair
-      const bool in = r == j && valid && b + u < u1 && cc * kChunk + 32 * q < w.K;
-      const f32x4* src = reinterpret_cast<const f32x4*>(h + (size_t)j * p.ldx + (size_t)cc * kChunk);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) xf[u][s] = in ? src[s] : f32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int i = 0; i < NT; ++i) s[i] = mx_scale<kBf16>(sc[u][i]);
+      const uint32_t mine = r == col[u] ? ~0u : 0u;  // the other columns are zero
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        frag hi, lo;
-        split_bf16(xf[u][2 * j], xf[u][2 * j + 1], hi, lo);
+        const frag hi = __builtin_bit_cast(frag, hs[wave][4 * q + j] & mine);
+        const frag lo = __builtin_bit_cast(frag, hs[wave][16 + 4 * q + j] & mine);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const frag a = T::decode(cd[u][i][j], mx_scale<kBf16>(sc[u][i]));
+          const frag a = T::decode(cd[u][i][j], s[i]);
           acc[i] = T::mfma(a, lo, acc[i]);
           acc[i] = T::mfma(a, hi, acc[i]);
         }
       }
+      wave_lds_order();
+      load(u, b + u + U);
+    }
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) red[wave][i][lane] = acc[i];
   __syncthreads();
-  // lane (q, j): the outputs n = 4q .. 4q + 3 of pair j; the sum over the
-  // pairs runs over the 16 lanes of a row in the order of j
+  // lane (q, j): the outputs n = 4q .. 4q + 3 of pair j, summed in the order of j
   for (int s = threadIdx.x; s < NT * 4; s += W * 64) {
     const int i = s >> 2, qq = s & 3;
     const int t = (int)blockIdx.x * NT + i;
@@ -266,30 +317,57 @@ __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
   }
 }
 
-template <int MODE, int W, int NT, int MT, int U>
+template <int MODE, int W, int NT, int RX, int U>
 hipError_t go(const MxParams& p, hipStream_t s) {
   constexpr bool kUp = MODE == kMxUp || MODE == kMxUpPair;
+  constexpr int kRows = (RX + 3) / 4 * 16;
   const int tiles = kUp ? p.w.ntile / 2 : p.w.ntile, per = kUp ? NT / 2 : NT;
-  const dim3 g((unsigned)((tiles + per - 1) / per), 1);
+  const unsigned gx = (unsigned)((tiles + per - 1) / per);
   MxParams q = p;
-  // grid.y holds 65535 at most
   if constexpr (MODE == kMxDense) {
-    const int step = 65535 * 16 * MT;
+    const int step = 65535 * kRows;  // grid.y
     for (int m0 = 0; m0 < p.M; m0 += step) {
       q.M = p.M - m0 < step ? p.M - m0 : step;
       q.x = static_cast<const uint16_t*>(p.x) + (size_t)m0 * p.ldx;
       q.y = static_cast<uint16_t*>(p.y) + (size_t)m0 * p.w.N;
-      const unsigned gy = (unsigned)((q.M + 16 * MT - 1) / (16 * MT));
-      mx_stream_kernel<MODE, W, NT, MT, U><<<dim3(g.x, gy), W * 64, 0, s>>>(q);
+      mx_stream_kernel<MODE, W, NT, RX, U>
+          <<<dim3(gx, (unsigned)((q.M + kRows - 1) / kRows)), W * 64, 0, s>>>(q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
   } else {
     const unsigned gy = MODE == kMxUpPair ? (unsigned)p.pairs : (unsigned)p.max_tiles;
-    mx_stream_kernel<MODE, W, NT, MT, U><<<dim3(g.x, gy), W * 64, 0, s>>>(q);
+    mx_stream_kernel<MODE, W, NT, RX, U><<<dim3(gx, gy), W * 64, 0, s>>>(q);
     return hipGetLastError();
   }
+}
+
+// Dense shapes. More weight tiles per workgroup share each activation
+// fragment: as many as leave about a workgroup per CU (us, 1 / 2 / 4 tiles:
+// 64 rows of 28672 x 8192 - / 79 / 52; 32 rows of 14336 x 4096 22.2 / 16.5 /
+// 12.6; of 4096 x 14336 19.5 / 22.2 / 28.5). One to four rows need no sharing:
+// there two tiles and four waves on a wide matrix (14336 x 4096: 8.4, one tile
+// and eight waves 8.7 to 10.1), one tile and eight waves on a narrow one
+// (4096 x 14336: 8.3 against 10.5 and more).
+template <int RX, int U4, int U1>
+hipError_t by_width(const MxParams& p, int cus, hipStream_t s) {
+  const int t = p.w.ntile;
+  if (5 * t >= 16 * cus) return go<kMxDense, 8, 4, RX, U4>(p, s);
+  if (5 * t >= 8 * cus) return go<kMxDense, 8, 2, RX, U4>(p, s);
+  return go<kMxDense, 8, 1, RX, U1>(p, s);
+}
+hipError_t dense(const MxParams& p, int cus, hipStream_t s) {
+  if (p.M <= 4) {
+    if (p.w.ntile >= 2 * cus) return go<kMxDense, 4, 2, 1, 4>(p, s);
+    // a short K leaves a wave few chunks: 1024 x 1024 2.8 with two in flight, 3.5 with four
+    return p.w.nchunk >= 64 ? go<kMxDense, 8, 1, 1, 4>(p, s) : go<kMxDense, 8, 1, 1, 2>(p, s);
+  }
+  if (p.M <= 8) return by_width<2, 2, 2>(p, cus, s);
+  if (p.M <= 16) return by_width<4, 2, 2>(p, cus, s);
+  if (p.M <= 32) return by_width<8, 2, 2>(p, cus, s);
+  if (p.M <= 48) return by_width<12, 1, 1>(p, cus, s);
+  return by_width<16, 1, 1>(p, cus, s);
 }
 
 }  // namespace
@@ -297,16 +375,12 @@ hipError_t go(const MxParams& p, hipStream_t s) {
 template <>
 hipError_t mx_stream<DT>(const MxParams& p, int mode, int cus, hipStream_t s) {
   switch (mode) {
-    case kMxDense:
-      if (p.M <= 16) return go<kMxDense, 8, 1, 1, 4>(p, s);
-      if (p.M <= 32) return go<kMxDense, 8, 2, 2, 2>(p, s);
-      return go<kMxDense, 8, 2, 4, 1>(p, s);
-    case kMxUp: return go<kMxUp, 8, 2, 1, 4>(p, s);
-    case kMxDown: return go<kMxDown, 8, 1, 1, 4>(p, s);
+    case kMxDense: return dense(p, cus, s);
+    case kMxUp: return go<kMxUp, 8, 2, 4, 4>(p, s);
+    case kMxDown: return go<kMxDown, 8, 1, 4, 2>(p, s);
     case kMxUpPair: return go<kMxUpPair, 8, 2, 1, 4>(p, s);
     default: {
-      const dim3 g((unsigned)p.w.ntile, (unsigned)p.M);
-      mx_down_token_kernel<8, 1, 4><<<g, 512, 0, s>>>(p);
+      mx_down_token_kernel<8, 1, 4><<<dim3((unsigned)p.w.ntile, (unsigned)p.M), 512, 0, s>>>(p);
       return hipGetLastError();
     }
   }

@@ -118,10 +118,11 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxParams p, int m
   auto step = [&](int c, const u32x4* cur, u32x4* next, const u32x4* d, const uint32_t* s, u32x4* dn,
                   uint32_t* sn) {
     __syncthreads();
-    if (c + 1 < w.nchunk) {
-      load_x(c + 1, next);
-      load_w(c + 1, dn, sn);
-    }
+    // (without a branch, across which the compiler would move the products
+    // away from their operands: past the last chunk it is fetched again)
+    const int cn = c + 1 < w.nchunk ? c + 1 : c;
+    load_x(cn, next);
+    load_w(cn, dn, sn);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       frag b[MI];

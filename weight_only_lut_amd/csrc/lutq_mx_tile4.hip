@@ -20,48 +20,49 @@ __device__ __forceinline__ i32x8 widen(u32x4 v) {
 }
 
 template <int DT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void mx_tile4_kernel(MxParams p, int mtiles) {
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, int mtiles) {
   constexpr int kWaves = WM * WN;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
-  constexpr int kStepChunks = 2;
-  constexpr int XB = BM / 16 * kStepChunks / kWaves, WB = BN / 16 * kStepChunks / kWaves;
-  __shared__ u32x4 xs[2][BM / 16 * kStepChunks][kWave];
-  __shared__ u32x4 ws[2][BN / 16 * kStepChunks][kWave];
+  constexpr int XL = BM / 8 / kWaves, WL = BN / 8 / kWaves;  // KiB per wave and step
+  __shared__ u32x4 xs0[BM * 8], xs1[BM * 8];
+  __shared__ u32x4 ws0[BN * 8], ws1[BN * 8];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
   const unsigned id = xcd_contiguous(blockIdx.x, gridDim.x);
   const int row0 = (int)(id % mtiles) * BM, nt = (int)(id / mtiles);
+  const int rows = p.M - row0 < BM ? p.M - row0 : BM;
   const MxWeights& w = p.w;
   const int kb = w.K / kMxBlock;
-  const uint8_t* x = static_cast<const uint8_t*>(p.x);
 
-  // LDS blocks this wave fetches: block b is tile b / 2, chunk b % 2 of the step
-  size_t xrow[XB], wtile[WB];
-#pragma unroll
-  for (int i = 0; i < XB; ++i) {
-    const int row = row0 + (wave * XB + i) / kStepChunks * 16 + r;
-    xrow[i] = (size_t)(row < p.M ? row : p.M - 1);
-  }
-#pragma unroll
-  for (int i = 0; i < WB; ++i) {
-    const int t = nt * (BN / 16) + (wave * WB + i) / kStepChunks;
-    wtile[i] = (size_t)(t < w.ntile ? t : w.ntile - 1);
-  }
-  // and the scales of the tiles it multiplies
-  size_t srow[MI];
-  uint32_t stile[NI];
-#pragma unroll
-  for (int m = 0; m < MI; ++m) {
-    const int row = row0 + (wm * MI + m) * 16 + r;
-    srow[m] = (size_t)(row < p.M ? row : p.M - 1) * kb;
-  }
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int t = nt * (BN / 16) + wn * NI + i;
-    stile[i] = (uint32_t)(t < w.ntile ? t : w.ntile - 1);
-  }
+  // Activations: a step of a row is 128 bytes, eight lanes of a load; its
+  // pieces are exchanged by the row's low bits, so that the rows a fragment
+  // read takes at a time lie in different banks. Rows past the last read as
+  // zeros.
+  const __amdgpu_buffer_rsrc_t xrs =
+      make_rsrc(static_cast<const uint8_t*>(p.x) + row0 * p.ldx, (uint32_t)(rows * p.ldx));
+  const int xrow = wave * XL * 8 + (lane >> 3), piece = (lane ^ (lane >> 3)) & 7;
+  const uint32_t xoff = (uint32_t)(xrow * p.ldx + piece * kMxSlotBytes);
+  const uint32_t xstep = (uint32_t)(8 * p.ldx);
+  // Weights: whole blocks; block i of a wave is tile i / 2, chunk i % 2. Tiles
+  // past the last are the last again: they are computed, not stored.
+  static_assert(WL % 2 == 0, "a wave fetches both chunks of its tiles");
+  const int tile0 = nt * (BN / 16), last = w.ntile - 1 - tile0;
+  const auto tile_at = [&](int t) { return (uint32_t)(t < last ? t : last); };
+  const __amdgpu_buffer_rsrc_t wrs =
+      make_rsrc(w.codes + (size_t)tile0 * w.nchunk * kMxBlockBytes, (uint32_t)(last + 1 < BN / 16 ? last + 1 : BN / 16) *
+                                                                        (uint32_t)w.nchunk * kMxBlockBytes);
+  // Scales of the tiles it multiplies: a lane's dword holds four chunks, two
+  // steps; the instructions pick the byte. Activations' tiles past the last
+  // read as zeros (2^-127).
+  const int mtile0 = row0 / 16, mlast = (p.M + 15) / 16 - mtile0;
+  const __amdgpu_buffer_rsrc_t srs =
+      make_rsrc(p.xscales + (size_t)mtile0 * w.nquad * (kWave * 4),
+                (uint32_t)(mlast < BM / 16 ? mlast : BM / 16) * (uint32_t)w.nquad * (kWave * 4));
+  const __amdgpu_buffer_rsrc_t vrs =
+      make_rsrc(w.scales + (size_t)tile0 * w.nquad * (kWave * 4), (uint32_t)(last + 1 < BN / 16 ? last + 1 : BN / 16) *
+                                                                      (uint32_t)w.nquad * (kWave * 4));
 
   f32x4 acc[NI][MI];
 #pragma unroll
@@ -69,76 +70,73 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile4_kernel(MxParams p, int 
 #pragma unroll
     for (int m = 0; m < MI; ++m) acc[i][m] = f32x4{0, 0, 0, 0};
 
-  const int steps = (w.nchunk + kStepChunks - 1) / kStepChunks;
-  u32x4 xr[XB], wr[WB];
-  uint32_t sx[2][MI][kStepChunks], sw[2][NI];
-  auto fetch = [&](int s, int stage) {
+  auto load = [&](int s, u32x4* xs, u32x4* ws) {
+    // a block past K: zero codes
+    const bool past = (s + 1) * 8 > kb && s * 8 + piece >= kb;
 #pragma unroll
-    for (int i = 0; i < XB; ++i) {
-      const int b = (s * kStepChunks + (wave * XB + i) % kStepChunks) * 4 + q;
-      const u32x4* src = reinterpret_cast<const u32x4*>(x + xrow[i] * p.ldx + (size_t)b * kMxSlotBytes);
-      xr[i] = *(b < kb ? src : &mx_zero16);
-    }
+    for (int i = 0; i < XL; ++i)
+      buffer_to_lds(xrs, past ? kOutOfRange : xoff + i * xstep + (uint32_t)s * 128, xs + (wave * XL + i) * kWave);
 #pragma unroll
-    for (int i = 0; i < WB; ++i) {
+    for (int i = 0; i < WL; ++i) {
       // a chunk past the last: any valid one, the activations are zero there
-      int c = s * kStepChunks + (wave * WB + i) % kStepChunks;
+      int c = 2 * s + i % 2;
       c = c < w.nchunk ? c : w.nchunk - 1;
-      wr[i] = *reinterpret_cast<const u32x4*>(w.codes + (wtile[i] * w.nchunk + c) * kMxBlockBytes +
-                                              lane * kMxSlotBytes);
+      buffer_to_lds(wrs, lane * kMxSlotBytes, ws + (wave * WL + i) * kWave,
+                    (tile_at(wave * (WL / 2) + i / 2) * w.nchunk + c) * kMxBlockBytes);
     }
+  };
+  uint32_t sx[MI], sw[NI], sxn[MI], swn[NI];
+  auto load_scales = [&](int quad, uint32_t* x, uint32_t* v) {
+    quad = quad < w.nquad ? quad : w.nquad - 1;
 #pragma unroll
     for (int m = 0; m < MI; ++m)
-#pragma unroll
-      for (int c = 0; c < kStepChunks; ++c) {
-        const int b = (s * kStepChunks + c) * 4 + q;
-        const uint32_t v = p.xscales[srow[m] + (b < kb ? b : kb - 1)];
-        sx[stage][m][c] = b < kb ? v : 127u;  // not a NaN of another block
-      }
+      x[m] = __builtin_amdgcn_raw_buffer_load_b32(
+          srs, ((uint32_t)(wm * MI + m) * w.nquad + quad) * (kWave * 4) + lane * 4, 0, 0);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      sw[stage][i] = *reinterpret_cast<const uint16_t*>(
-          w.scales + ((size_t)stile[i] * w.nquad + s / 2) * (kWave * 4) + lane * 4 + (s & 1) * 2);
+      v[i] = __builtin_amdgcn_raw_buffer_load_b32(
+          vrs, lane * 4, (tile_at(wn * NI + i) * w.nquad + quad) * (kWave * 4), 0);
   };
-  auto put = [&](int stage) {
-#pragma unroll
-    for (int i = 0; i < XB; ++i) xs[stage][wave * XB + i][lane] = xr[i];
-#pragma unroll
-    for (int i = 0; i < WB; ++i) ws[stage][wave * WB + i][lane] = wr[i];
-  };
-  fetch(0, 0);
-  put(0);
-  auto step = [&](int s, int stage) {
-    __syncthreads();
-    const bool more = s + 1 < steps;
-    if (more) fetch(s + 1, stage ^ 1);
-#pragma unroll
-    for (int c = 0; c < kStepChunks; ++c) {
-      i32x8 b[MI];
-#pragma unroll
-      for (int m = 0; m < MI; ++m) b[m] = widen(xs[stage][(wm * MI + m) * kStepChunks + c][lane]);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const i32x8 a = widen(ws[stage][(wn * NI + i) * kStepChunks + c][lane]);
-#pragma unroll
-        for (int m = 0; m < MI; ++m) {
-          if (c == 0)
-            acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                a, b[m], acc[i][m], 4, 4, 0, (int)sw[stage][i], 0, (int)sx[stage][m][c]);
-          else
-            acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                a, b[m], acc[i][m], 4, 4, 1, (int)sw[stage][i], 0, (int)sx[stage][m][c]);
-        }
-      }
-    }
-    if (more) put(stage ^ 1);
-  };
-  int s = 0;
-  for (; s + 1 < steps; s += 2) {
-    step(s, 0);
-    step(s + 1, 1);
+  // One step (the H-th of its quad): the next one's tiles go out first. The
+  // barrier also waits for this step's tiles, and for every wave to be done
+  // with the other stage. (The fetch is not conditional: the compiler would
+  // move the products away from their operands across the branch. Past the
+  // last step the activations are out of range.)
+#define LUTQ_STEP(H, s, xs, ws, xn, wnx)                                                            \
+  {                                                                                                 \
+    __syncthreads();                                                                                \
+    load((s) + 1, xn, wnx);                                                                         \
+    _Pragma("unroll") for (int c = 0; c < 2; ++c) {                                                 \
+      __builtin_amdgcn_sched_barrier(0);                                                            \
+      i32x8 b[MI];                                                                                  \
+      _Pragma("unroll") for (int m = 0; m < MI; ++m)                                                \
+          b[m] = widen(xs[((wm * MI + m) * 16 + r) * 8 + ((c * 4 + q) ^ (r & 7))]);                 \
+      _Pragma("unroll") for (int i = 0; i < NI; ++i) {                                              \
+        const i32x8 a = widen(ws[((wn * NI + i) * 2 + c) * kWave + lane]);                          \
+        _Pragma("unroll") for (int m = 0; m < MI; ++m) {                                            \
+          if (c == 0)                                                                               \
+            acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                           \
+                a, b[m], acc[i][m], 4, 4, 2 * H, (int)sw[i], 2 * H, (int)sx[m]);                    \
+          else                                                                                      \
+            acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                           \
+                a, b[m], acc[i][m], 4, 4, 2 * H + 1, (int)sw[i], 2 * H + 1, (int)sx[m]);            \
+        }                                                                                           \
+      }                                                                                             \
+    }                                                                                               \
+    __builtin_amdgcn_sched_barrier(0);                                                              \
   }
-  if (s < steps) step(s, 0);
+  load(0, xs0, ws0);
+  load_scales(0, sx, sw);
+  for (int quad = 0; quad < w.nquad; ++quad) {
+    load_scales(quad + 1, sxn, swn);
+    LUTQ_STEP(0, 2 * quad, xs0, ws0, xs1, ws1)
+    LUTQ_STEP(1, 2 * quad + 1, xs1, ws1, xs0, ws0)
+#pragma unroll
+    for (int m = 0; m < MI; ++m) sx[m] = sxn[m];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) sw[i] = swn[i];
+  }
+#undef LUTQ_STEP
 
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -155,6 +153,29 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile4_kernel(MxParams p, int 
   }
 }
 
+// The activations' scale bytes [M][K/32] in the order of the packed weights'
+// scales, zeros past M and K: a wave reads a tile's scales of four chunks as
+// one run. (Read as they are, a byte per lane from 16 rows, they took longer
+// than the products: 1.6 PFLOP/s at most.)
+__global__ __launch_bounds__(256) void mx_scale_tiles_kernel(const uint8_t* scales, int M, int kb,
+                                                              int nquad, uint32_t* out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // dword: (tile, quad, slot)
+  const long long tq = i >> 6;
+  const int slot = (int)(i & 63), quad = (int)(tq % nquad);
+  const long long row = tq / nquad * 16 + (slot & 15);
+  if (row / 16 * 16 >= M) return;
+  uint32_t v = 0;
+  if (row < M) {
+    const uint8_t* s = scales + row * kb;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int b = (quad * 4 + c) * 4 + (slot >> 4);
+      if (b < kb) v |= (uint32_t)s[b] << (8 * c);
+    }
+  }
+  out[i] = v;
+}
+
 template <int DT, int BM, int BN, int WM, int WN>
 hipError_t go(const MxParams& p, hipStream_t s) {
   const long long mt = (p.M + BM - 1) / BM, nt = (p.w.ntile + BN / 16 - 1) / (BN / 16);
@@ -166,13 +187,21 @@ hipError_t go(const MxParams& p, hipStream_t s) {
 template <int DT>
 hipError_t pick(const MxParams& p, int cus, hipStream_t s) {
   if (p.M <= 64) return go<DT, 64, 128, 2, 4>(p, s);
-  return go<DT, 256, 256, 2, 4>(p, s);
+  return go<DT, 256, 256, 4, 2>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_mx_tile4(const MxParams& p, int dtype, int cus, hipStream_t s) {
-  return dtype == kF16 ? pick<kF16>(p, cus, s) : pick<kBf16>(p, cus, s);
+  const int nquad = p.w.nquad;
+  const long long n = (long long)mx_scale_tile_bytes(p.M, p.w.K) / 4;
+  mx_scale_tiles_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
+      p.xscales, p.M, p.w.K / kMxBlock, nquad, static_cast<uint32_t*>(p.workspace));
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  MxParams q = p;
+  q.xscales = static_cast<const uint8_t*>(p.workspace);
+  return dtype == kF16 ? pick<kF16>(q, cus, s) : pick<kBf16>(q, cus, s);
 }
 
 }  // namespace lutq
