@@ -59,9 +59,22 @@ def declare(lib):
         fn.argtypes, fn.restype = args, res
 
 
-def _raw_stream(device):
-    """The current stream's handle, as an int."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+# The current stream's handle of a device index, as an int.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _new(rows, cols, dtype, device):
+    """An uninitialized contiguous matrix (the cheapest way to have one:
+    1.3 us against torch.empty's 1.7, of a call's 7)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _gpu(index, *tensors):
+    """Checks that every tensor is on GPU `index` (of the first), and returns it."""
+    for name, t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _on_device(*tensors)        # says which one is not
+    return index
 
 
 def _rows_of(t, name, types):
@@ -101,12 +114,12 @@ def mx_quantize(x, rule: str = "floor"):
     rows, K = x.shape
     if K % MX_BLOCK:
         raise ValueError(f"K = {K} is not a multiple of {MX_BLOCK}")
-    _on_device(("x", x))
+    gpu = _gpu(x.get_device(), ("x", x))
     dev = x.device
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((rows, K // MX_BLOCK), dtype=torch.uint8, device=dev)
+    codes = _new(rows, K // 2, torch.uint8, dev)
+    scales = _new(rows, K // MX_BLOCK, torch.uint8, dev)
     rc = _lib().lutq_mx_quantize(x.data_ptr(), _TYPES[x.dtype], rows, K, ldx, _RULES[rule],
-                                 codes.data_ptr(), scales.data_ptr(), _raw_stream(dev))
+                                 codes.data_ptr(), scales.data_ptr(), _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_mx_quantize")
     return codes, scales
@@ -117,13 +130,14 @@ def mx_dequantize(codes, scales, dtype=torch.bfloat16):
     codes, scales = _codes_of((codes, scales), "mx")
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be {' or '.join(str(d) for d in _TYPES)}, got {dtype}")
-    _on_device(("codes", codes), ("scales", scales))
+    gpu = _gpu(codes.get_device(), ("codes", codes), ("scales", scales))
     dev = codes.device
     K = codes.shape[-1] * 2
-    rows = codes.numel() * 2 // K if K else 0
-    x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=dev)
+    rows = codes.shape[0] if codes.dim() == 2 else codes.numel() * 2 // K if K else 0
+    x = _new(rows, K, dtype, dev) if codes.dim() == 2 else torch.empty((*codes.shape[:-1], K), dtype=dtype,
+                                                                       device=dev)
     rc = _lib().lutq_mx_dequantize(codes.data_ptr(), scales.data_ptr(), _TYPES[dtype], rows, K,
-                                   x.data_ptr(), _raw_stream(dev))
+                                   x.data_ptr(), _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_mx_dequantize")
     return x
@@ -149,14 +163,14 @@ def mx_pack(codes, scales) -> MxPacked:
     codes, scales = _codes_of((codes, scales), "weight")
     if codes.dim() > 3:
         raise ValueError("codes must be [N, K/2] or [experts, N, K/2]")
-    _on_device(("codes", codes), ("scales", scales))
+    gpu = _gpu(codes.get_device(), ("codes", codes), ("scales", scales))
     E = codes.shape[0] if codes.dim() == 3 else 1
     N, K = codes.shape[-2], codes.shape[-1] * 2
     nbytes = _lib().lutq_mx_packed_bytes(E, N, K)
     dst = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=codes.device)
     desc = MxPackedDesc()
     rc = _lib().lutq_mx_pack(codes.data_ptr(), scales.data_ptr(), E, N, K, dst.data_ptr(), dst.numel(),
-                             ctypes.addressof(desc), _raw_stream(codes.device))
+                             ctypes.addressof(desc), _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_mx_pack")
     return MxPacked(dst, desc)
@@ -195,23 +209,23 @@ def mx_matmul(x, p: MxPacked, *, dtype=None, path: str = "auto", out=None):
         raise ValueError(f"x has K = {K}, the packed matrix K = {p.K}")
     if out is not None:
         _check(out, "out", dtype, shape=(M, p.N))
+    first = xc if four else x
     if four:
-        _on_device(("x codes", xc), ("x scales", xs), ("packed data", p.data), ("out", out))
-        dev = xc.device
+        gpu = _gpu(xc.get_device(), ("x codes", xc), ("x scales", xs), ("packed data", p.data), ("out", out))
     else:
-        _on_device(("x", x), ("packed data", p.data), ("out", out))
-        dev = x.device
+        gpu = _gpu(x.get_device(), ("x", x), ("packed data", p.data), ("out", out))
     if out is None:
-        out = torch.empty((M, p.N), dtype=dtype, device=dev)
+        out = _new(M, p.N, dtype, first.device)
     lib = _lib()
     nbytes = lib.lutq_mx_workspace_bytes(M, p.N, K, four)
-    space = torch.empty(nbytes, dtype=torch.uint8, device=dev).data_ptr() if nbytes else None
+    space = _new(1, nbytes, torch.uint8, first.device) if nbytes else None
+    at = space.data_ptr() if nbytes else None
     if four:
         rc = lib.lutq_mx_matmul_mx(xc.data_ptr(), xs.data_ptr(), p._ref, out.data_ptr(), _HALF[dtype], M,
-                                   p.N, K, space, nbytes, _raw_stream(dev))
+                                   p.N, K, at, nbytes, _raw_stream(gpu))
     else:
         rc = lib.lutq_mx_matmul(x.data_ptr(), _HALF[dtype], ldx, p._ref, out.data_ptr(), M, p.N, K,
-                                _PATHS[path], space, nbytes, _raw_stream(dev))
+                                _PATHS[path], at, nbytes, _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_mx_matmul")
     return out
@@ -246,17 +260,16 @@ def moe_route(logits, k: int, *, score: str = "softmax", bias=None, groups: int 
     T, E = logits.shape
     if bias is not None:
         _check(bias, "bias", torch.float32, shape=(E,))
-    _on_device(("logits", logits), ("bias", bias))
-    dev = logits.device
-    ints = _lib().lutq_moe_plan_ints(T, E, k)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-    plan = torch.empty(ints, dtype=torch.int32, device=dev)
+    gpu = _gpu(logits.get_device(), ("logits", logits), ("bias", bias))
+    dev, lib = logits.device, _lib()
+    ints = lib.lutq_moe_plan_ints(T, E, k)
+    ids = _new(T, max(k, 0), torch.int32, dev)
+    weights = _new(T, max(k, 0), torch.float32, dev)
+    plan = torch.empty_strided((ints,), (1,), dtype=torch.int32, device=dev)
     o = MoeOptions(_SCORES[score], groups, top_groups, group_best, int(bool(renorm)), scale)
-    rc = _lib().lutq_moe_route(logits.data_ptr(), _TYPES[logits.dtype], ld,
-                               None if bias is None else bias.data_ptr(), T, E, k, ctypes.addressof(o),
-                               ids.data_ptr(), weights.data_ptr(), plan.data_ptr() or None,
-                               _raw_stream(dev))
+    rc = lib.lutq_moe_route(logits.data_ptr(), _TYPES[logits.dtype], ld,
+                            None if bias is None else bias.data_ptr(), T, E, k, ctypes.addressof(o),
+                            ids.data_ptr(), weights.data_ptr(), plan.data_ptr() or None, _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_moe_route")
     return Routing(ids, weights, plan, E)
@@ -269,10 +282,10 @@ def moe_plan(ids, weights, experts: int) -> Routing:
     if ids.dim() != 2:
         raise ValueError("ids must be a 2-D tensor [T, k]")
     _check(weights, "weights", torch.float32, shape=ids.shape)
-    _on_device(("ids", ids), ("weights", weights))
+    gpu = _gpu(ids.get_device(), ("ids", ids), ("weights", weights))
     T, k = ids.shape
     plan = torch.empty(_lib().lutq_moe_plan_ints(T, experts, k), dtype=torch.int32, device=ids.device)
-    rc = _lib().lutq_moe_plan(ids.data_ptr(), T, experts, k, plan.data_ptr() or None, _raw_stream(ids.device))
+    rc = _lib().lutq_moe_plan(ids.data_ptr(), T, experts, k, plan.data_ptr() or None, _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_moe_plan")
     return Routing(ids, weights, plan, experts)
@@ -298,18 +311,18 @@ def moe_mlp(x, gate_up: MxPacked, down: MxPacked, routing: Routing, *, out=None)
                          f"expected {T} over {E}")
     if out is not None:
         _check(out, "out", x.dtype, shape=(T, D))
-    _on_device(("x", x), ("gate_up data", gate_up.data), ("down data", down.data),
+    gpu = _gpu(x.get_device(), ("x", x), ("gate_up data", gate_up.data), ("down data", down.data),
                ("routing", routing.plan), ("out", out))
     dev = x.device
     k = routing.ids.shape[1]
     lib = _lib()
     nbytes = lib.lutq_moe_workspace_bytes(T, k, D, F)
-    space = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    space = _new(1, nbytes, torch.uint8, dev)
     if out is None:
-        out = torch.empty((T, D), dtype=x.dtype, device=dev)
+        out = _new(T, D, x.dtype, dev)
     rc = lib.lutq_moe_mlp(x.data_ptr(), _HALF[x.dtype], ldx, gate_up._ref, down._ref,
                           routing.ids.data_ptr(), routing.weights.data_ptr(), routing.plan.data_ptr(), T, k,
-                          space.data_ptr(), nbytes, out.data_ptr(), _raw_stream(dev))
+                          space.data_ptr(), nbytes, out.data_ptr(), _raw_stream(gpu))
     if rc:
         raise LutqError(rc, "lutq_moe_mlp")
     return out

@@ -2,16 +2,17 @@
 // their weights; the plan that groups the (token, choice) pairs by expert; and
 // the sum of the experts' outputs per token.
 //
-// One wave routes a token: lane l holds the experts l, l + 64, ... in
-// registers, so that the logits are read once, coalesced, and a choice is a
-// wave maximum over order-preserving integer keys (four DPP steps, then scalar
-// code) and a ballot for the lowest expert that has it.
+// One wave routes a token: each lane holds E / 64 neighbouring experts, sorted
+// by order-preserving integer keys, so that the logits are read once and a
+// choice is a wave maximum over the lanes' first keys (four DPP steps, then
+// scalar code) and a ballot for the lowest lane that has it.
 //
-// The plan is a stable counting sort. Up to 1024 pairs one workgroup routes
-// and plans in a single launch, since there the launches are the time; beyond
-// that, segments of 2048 pairs are counted, the counts scanned, and each
-// segment places its pairs. Ranks come from ballots, never from the order in
-// which atomics happen to land.
+// The plan is a stable counting sort. Up to 64 pairs a single wave plans by
+// comparing every pair with every other, up to 1024 one workgroup sorts, both
+// in the launch that routes, since there the launches are the time. Beyond
+// that, segments of 2048 pairs are counted, and each segment places its pairs
+// behind those of earlier ones. Ranks come from ballots, never from the order
+// in which atomics happen to land.
 #include "lutq_mx_device.h"
 
 namespace lutq {
@@ -60,8 +61,8 @@ __device__ __forceinline__ float load_logit(const RouteParams& p, long long at) 
   return __builtin_bit_cast(float, (uint32_t)h << 16);
 }
 
-// The groups kept of the experts' keys in `keys` (LDS, -infinity for experts
-// never chosen), as a mask.
+// The groups kept, as a mask, of the experts' keys in `keys` (LDS, -infinity
+// for experts never chosen).
 __device__ uint64_t choose_groups(const RouteParams& p, const float* keys, int lane) {
   const float kNone = -__builtin_inff();
   int slots = 1;  // lanes per group
@@ -93,107 +94,103 @@ __device__ uint64_t choose_groups(const RouteParams& p, const float* keys, int l
   return kept;
 }
 
-// Routes token t with one wave; the ids also go to `ids_out` (LDS or global).
+// Routes token t with one wave; the ids also go to `ids_out` (LDS), if given.
 // `keys` is E floats of LDS of this wave, used with groups only.
 template <int VPT>
 __device__ void route_token(const RouteParams& p, int t, int lane, float* keys, int32_t* ids_out) {
   const float kNone = -__builtin_inff();
-  float logit[VPT], score[VPT];
-  uint32_t key[VPT];
+  const long long row = t * p.ld;
+  const int e0 = lane * VPT;
+  float logit[VPT], kf[VPT];
 #pragma unroll
-  for (int s = 0; s < VPT; ++s) {
-    const int e = s * kWave + lane;
-    logit[s] = e < p.E ? load_logit(p, t * p.ld + e) : kNone;
-  }
+  for (int s = 0; s < VPT; ++s) logit[s] = e0 + s < p.E ? load_logit(p, row + e0 + s) : kNone;
+  const bool by_logit = !p.bias && (p.groups == 1 || p.group_best == 1);
   bool bad = false;  // a NaN or +infinity in a softmax row
-  float top = kNone, total = 1.0f;
+  float top = 0.0f, total = 1.0f;
   if (!p.sigmoid) {
 #pragma unroll
-    for (int s = 0; s < VPT; ++s) {
-      bad |= !(logit[s] < __builtin_inff());
-      top = fmaxf(top, logit[s]);
-    }
+    for (int s = 0; s < VPT; ++s) bad |= !(logit[s] < __builtin_inff());
     bad = __ballot(bad) != 0;
-    top = unordered(wave_max_u32(ordered(top)));
-    total = 0.0f;
+    if (!(by_logit && p.renorm)) {  // the sum over all experts counts
+      top = kNone;
 #pragma unroll
-    for (int s = 0; s < VPT; ++s) {
-      score[s] = logit[s] == kNone ? 0.0f : expf(logit[s] - top);
-      total += score[s];
+      for (int s = 0; s < VPT; ++s) top = fmaxf(top, logit[s]);
+      top = unordered(wave_max_u32(ordered(top)));
+      total = 0.0f;
+#pragma unroll
+      for (int s = 0; s < VPT; ++s) total += logit[s] == kNone ? 0.0f : expf(logit[s] - top);
+      total = wave_sum(total);
     }
-    total = wave_sum(total);
-  } else {
-#pragma unroll
-    for (int s = 0; s < VPT; ++s) score[s] = 1.0f / (1.0f + expf(-logit[s]));
   }
-  const bool by_logit = !p.bias && (p.groups == 1 || p.group_best == 1);
-  float kf[VPT];
 #pragma unroll
   for (int s = 0; s < VPT; ++s) {
-    const int e = s * kWave + lane;
     float k = logit[s];
-    if (!by_logit && e < p.E) {
-      k = p.sigmoid ? score[s] : score[s] / total;
-      if (p.bias) k += p.bias[e];
+    if (!by_logit) {
+      k = p.sigmoid ? 1.0f / (1.0f + expf(-k)) : expf(k - top) / total;
+      if (p.bias && e0 + s < p.E) k += p.bias[e0 + s];
     }
-    if (logit[s] == kNone || k != k) k = kNone;
-    kf[s] = k;
+    kf[s] = logit[s] == kNone || k != k ? kNone : k;
   }
   uint64_t kept = ~0ull;
+  // e / size of e < 1024 is e * magic >> 20: too large by less than 1 / size
+  const uint32_t magic = p.group_magic;
   if (p.groups > 1) {
 #pragma unroll
     for (int s = 0; s < VPT; ++s)
-      if (s * kWave + lane < p.E) keys[s * kWave + lane] = kf[s];
+      if (e0 + s < p.E) keys[e0 + s] = kf[s];
     wave_lds_order();
     kept = choose_groups(p, keys, lane);
     wave_lds_order();
   }
-  const int size = p.E / p.groups;
+  // The lane's keys in falling order (0: never chosen), equal ones by expert:
+  // a choice is the largest of the lanes' first keys, in the lowest lane.
+  uint32_t key[VPT];
+  int which[VPT];
 #pragma unroll
   for (int s = 0; s < VPT; ++s) {
     key[s] = kf[s] == kNone ? 0u : ordered(kf[s]);
-    if (p.groups > 1 && !(kept >> ((s * kWave + lane) / size & 63) & 1)) key[s] = 0;
+    if (p.groups > 1 && !(kept >> ((uint32_t)(e0 + s) * magic >> 20 & 63) & 1)) key[s] = 0;
+    which[s] = e0 + s;
   }
-  // choice j ends in lane j
-  int id = -1;
-  float mine = 0.0f;  // its logit (softmax) or score
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t m = key[0];
 #pragma unroll
-    for (int s = 1; s < VPT; ++s) m = m > key[s] ? m : key[s];
-    m = wave_max_u32(m);
-    if (m == 0) break;
-    int at = -1;
-    float v = 0.0f;
+  for (int pass = 0; pass < VPT; ++pass)
 #pragma unroll
-    for (int s = 0; s < VPT; ++s) {
-      if (at < 0) {
-        const uint64_t b = __ballot(key[s] == m);
-        if (b) {
-          const int l = __builtin_ctzll(b);
-          at = s * kWave + l;
-          v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(
-                  __builtin_bit_cast(int, p.sigmoid ? score[s] : logit[s]), l));
-          if (lane == l) key[s] = 0;
-        }
-      }
+    for (int s = 0; s + 1 < VPT - pass; ++s) {
+      const bool swap = key[s + 1] > key[s];
+      const uint32_t k0 = key[s], k1 = key[s + 1];
+      const int w0 = which[s], w1 = which[s + 1];
+      key[s] = swap ? k1 : k0;
+      key[s + 1] = swap ? k0 : k1;
+      which[s] = swap ? w1 : w0;
+      which[s + 1] = swap ? w0 : w1;
     }
-    if (lane == j) {
-      id = at;
-      mine = v;
+  int id = -1;  // choice j in lane j
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t m = wave_max_u32(key[0]);
+    if (m == 0) break;
+    const int l = __builtin_ctzll(__ballot(key[0] == m));
+    const int at = __builtin_amdgcn_readlane(which[0], l);
+    if (lane == j) id = at;
+    if (lane == l) {
+#pragma unroll
+      for (int s = 0; s + 1 < VPT; ++s) {
+        key[s] = key[s + 1];
+        which[s] = which[s + 1];
+      }
+      key[VPT - 1] = 0;
     }
   }
   float w = 0.0f;
+  const float mine = id >= 0 ? load_logit(p, row + id) : kNone;
   if (p.sigmoid) {
-    w = id >= 0 ? mine : 0.0f;
+    w = id >= 0 ? 1.0f / (1.0f + expf(-mine)) : 0.0f;
     if (p.renorm) w = w / (wave_sum(w) + 1e-20f);
   } else {
-    // with renorm the chosen are measured from the first, the largest unless
-    // a bias reordered them
+    // with renorm the chosen are measured from the largest of them
     const float ref = p.renorm ? unordered(wave_max_u32(id >= 0 ? ordered(mine) : 0u)) : top;
     w = id >= 0 ? expf(mine - ref) : 0.0f;
     const float sum = p.renorm ? wave_sum(w) : total;
-    w = id < 0 ? 0.0f : bad ? __builtin_nanf("") : w / sum;
+    w = bad ? __builtin_nanf("") : w / sum;
   }
   if (lane < p.k) {
     const size_t at = (size_t)t * p.k + lane;
@@ -246,17 +243,17 @@ __device__ int block_scan(int* v, int n, int* tmp) {
   return total;
 }
 
-// Offsets and row tiles from the experts' counts in LDS (`cnt`, which become
-// the offsets). `aux` holds E ints, `tmp` THREADS / 64.
+// Offsets and row tiles of a plan, from the offsets in LDS. `aux` holds E
+// ints, `tmp` THREADS / 64.
 template <int THREADS>
-__device__ void write_offsets_and_tiles(int* cnt, int* aux, int* tmp, int E, int rows, int32_t* plan,
-                                        int32_t* tiles) {
-  for (int e = threadIdx.x; e < E; e += THREADS) aux[e] = (cnt[e] + rows - 1) / rows;
+__device__ void write_tiles(const int* offsets, int total, int* aux, int* tmp, int E, int rows,
+                            int32_t* plan, int32_t* tiles) {
+  const auto count = [&](int e) { return (e + 1 < E ? offsets[e + 1] : total) - offsets[e]; };
+  for (int e = threadIdx.x; e < E; e += THREADS) aux[e] = (count(e) + rows - 1) / rows;
   __syncthreads();
-  const int total = block_scan<THREADS>(cnt, E, tmp);
   const int ntiles = block_scan<THREADS>(aux, E, tmp);
   for (int e = threadIdx.x; e < E; e += THREADS) {
-    const int b = cnt[e], n = (e + 1 < E ? cnt[e + 1] : total) - b;
+    const int b = offsets[e], n = count(e);
     plan[e] = b;
     int32_t* out = tiles + 4 + 4 * (size_t)aux[e];
     for (int i = 0; i < n; i += rows, out += 4) {
@@ -326,6 +323,48 @@ __device__ void count_pairs(int* run, int E, int b, int n, Id id_of) {
   __syncthreads();
 }
 
+// At most 64 pairs: a wave per token routes (unless VPT is 0), then the first
+// wave finds each pair's position by counting the pairs before it. No row
+// tiles: the products of so few pairs do not use them.
+constexpr int kTinyPairs = kWave;
+constexpr int kTinyWaves = 16;
+
+template <int VPT>
+__global__ __launch_bounds__(kTinyWaves * 64) void moe_tiny_kernel(RouteParams p, MoePlanLayout l) {
+  __shared__ float keys[kTinyWaves][VPT > 0 ? VPT * kWave : 1];
+  __shared__ int32_t ids[kTinyPairs];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = p.T * p.k, waves = blockDim.x >> 6;
+  if constexpr (VPT > 0) {
+    for (int t = wave; t < p.T; t += waves) route_token<VPT>(p, t, lane, keys[wave], ids + t * p.k);
+    if (!p.plan) return;
+    __syncthreads();
+  } else {
+    if (lane < n) ids[lane] = p.ids[lane];
+    wave_lds_order();
+  }
+  if (wave) return;
+  int e = lane < n ? ids[lane] : -1;
+  if ((unsigned)e >= (unsigned)p.E) e = -1;
+  int at = 0;  // position: pairs of lower experts, and earlier ones of this
+  for (int j = 0; j < n; ++j) {
+    const int o = __builtin_amdgcn_readlane(e, j);
+    at += o >= 0 && (o < e || (o == e && j < lane));
+  }
+  const int live = __builtin_popcountll(__ballot(e >= 0));
+  int32_t* order = p.plan + l.order;
+  if (e >= 0) order[at] = lane;
+  if (lane >= live && lane < n) order[lane] = -1;
+  for (int b = lane; b <= p.E; b += kWave) {
+    int c = 0;
+    for (int j = 0; j < n; ++j) {
+      const int o = __builtin_amdgcn_readlane(e, j);
+      c += o >= 0 && o < b;
+    }
+    p.plan[b] = c;
+  }
+}
+
 constexpr int kSmallWaves = 16;
 
 // Few pairs: one workgroup routes (unless VPT is 0) and plans.
@@ -357,17 +396,14 @@ __global__ __launch_bounds__(kSmallWaves * 64) void moe_small_kernel(RouteParams
     cnt[e] = c;
   }
   __syncthreads();
-  write_offsets_and_tiles<kSmallWaves * 64>(cnt, aux, tmp, E, tile_rows, p.plan, p.plan + l.tiles);
+  const int live = block_scan<kSmallWaves * 64>(cnt, E, tmp);
+  write_tiles<kSmallWaves * 64>(cnt, live, aux, tmp, E, tile_rows, p.plan, p.plan + l.tiles);
   int32_t* order = p.plan + l.order;
-  int live = 0;  // as plan[E]
-  for (int w = 0; w < kSmallWaves; ++w) live += run[w * E + E - 1];
-  live += cnt[E - 1];
-  __syncthreads();
   place_pairs<kSmallWaves>(run, E, 0, n, [&](int e) { return cnt[e]; }, id_of, order);
   for (int i = live + threadIdx.x; i < n; i += kSmallWaves * 64) order[i] = -1;
 }
 
-constexpr int kSegWaves = 4;
+constexpr int kSegWaves = 8;
 
 __global__ __launch_bounds__(kSegWaves * 64) void moe_count_kernel(const int32_t* ids, int pairs, int E,
                                                                     int32_t* counts) {
@@ -410,22 +446,60 @@ __global__ __launch_bounds__(1024) void moe_scan_kernel(int32_t* counts, int seg
     cnt[e] = run;
   }
   __syncthreads();
-  write_offsets_and_tiles<1024>(cnt, aux, tmp, E, tile_rows, plan, tiles);
+  const int live = block_scan<1024>(cnt, E, tmp);
+  write_tiles<1024>(cnt, live, aux, tmp, E, tile_rows, plan, tiles);
 }
 
+// FUSED: the offsets and what earlier segments hold come from the counts
+// here (32 segments of 256 experts: 32 KB per workgroup, and a launch less);
+// the first workgroup writes offsets and row tiles.
+template <bool FUSED>
 __global__ __launch_bounds__(kSegWaves * 64) void moe_place_kernel(const int32_t* ids, int pairs, int E,
-                                                                    const int32_t* counts,
-                                                                    const int32_t* plan, int32_t* order) {
+                                                                    const int32_t* counts, int segments,
+                                                                    int tile_rows, int32_t* plan,
+                                                                    int32_t* tiles, int32_t* order) {
   extern __shared__ int lds[];
+  constexpr int kThreads = kSegWaves * 64;
+  int* run = lds;                    // [kSegWaves][E]
+  int* cnt = run + kSegWaves * E;    // FUSED: [E] offsets
+  int* before = cnt + E;             // FUSED: [E]
+  int* tmp = before + E;
   const int b = blockIdx.x * kPlanSegment, n = pairs - b < kPlanSegment ? pairs - b : kPlanSegment;
   const auto id_of = [&](int i) { return ids[i]; };
-  count_pairs<kSegWaves>(lds, E, b, n, id_of);
-  place_pairs<kSegWaves>(lds, E, b, n,
-                         [&](int e) { return plan[e] + counts[(size_t)blockIdx.x * E + e]; }, id_of,
-                         order);
+  count_pairs<kSegWaves>(run, E, b, n, id_of);
+  int live;
+  if constexpr (FUSED) {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      int total = 0, earlier = 0;
+      for (int s0 = 0; s0 < segments; s0 += 8) {
+        int c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = s0 + i < segments ? counts[(size_t)(s0 + i) * E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          total += c[i];
+          if (s0 + i < (int)blockIdx.x) earlier += c[i];
+        }
+      }
+      cnt[e] = total;
+      before[e] = earlier;
+    }
+    __syncthreads();
+    live = block_scan<kThreads>(cnt, E, tmp);
+    place_pairs<kSegWaves>(run, E, b, n, [&](int e) { return cnt[e] + before[e]; }, id_of, order);
+  } else {
+    live = plan[E];
+    place_pairs<kSegWaves>(run, E, b, n, [&](int e) { return plan[e] + counts[(size_t)blockIdx.x * E + e]; },
+                           id_of, order);
+  }
   // positions past the last pair
-  for (int i = b + threadIdx.x; i < b + n; i += kSegWaves * 64)
-    if (i >= plan[E]) order[i] = -1;
+  for (int i = b + threadIdx.x; i < b + n; i += kThreads)
+    if (i >= live) order[i] = -1;
+  if constexpr (FUSED) {
+    if (blockIdx.x) return;
+    __syncthreads();
+    write_tiles<kThreads>(cnt, live, before, tmp, E, tile_rows, plan, tiles);
+  }
 }
 
 // y[t] = the pair outputs of token t summed in the order of j, in fp32.
@@ -460,9 +534,17 @@ bool small_plan(int E, long long pairs) {
   return pairs <= kPlanSmallPairs && small_lds(E, (int)pairs) <= 64u * 1024;
 }
 
+// The same for one wave: the products then run without row tiles.
+bool tiny_plan(int T, int E, int k) {
+  return (long long)T * k <= kTinyPairs && moe_direct((long long)T * k, k, E);
+}
+
 template <int VPT>
 hipError_t route(const RouteParams& p, bool small, hipStream_t s) {
-  if (small) {
+  if (tiny_plan(p.T, p.E, p.k)) {
+    const int waves = p.T < kTinyWaves ? p.T : kTinyWaves;
+    moe_tiny_kernel<VPT><<<1, waves * 64, 0, s>>>(p, moe_plan_layout(p.T, p.E, p.k));
+  } else if (small) {
     const MoePlanLayout l = moe_plan_layout(p.T, p.E, p.k);
     moe_small_kernel<VPT><<<1, kSmallWaves * 64, small_lds(p.E, p.T * p.k), s>>>(
         p, l, moe_tile_rows((long long)p.T * p.k, p.E));
@@ -477,31 +559,39 @@ hipError_t route(const RouteParams& p, bool small, hipStream_t s) {
 hipError_t launch_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, hipStream_t s) {
   const MoePlanLayout l = moe_plan_layout(T, E, k);
   const int pairs = T * k, rows = moe_tile_rows(pairs, E);
-  if (small_plan(E, pairs)) {
+  if (small_plan(E, pairs) || tiny_plan(T, E, k)) {
     RouteParams p = {};
     p.T = T;
     p.E = E;
     p.k = k;
     p.ids = const_cast<int32_t*>(ids);
     p.plan = plan;
-    moe_small_kernel<0><<<1, kSmallWaves * 64, small_lds(E, pairs), s>>>(p, l, rows);
+    if (pairs > 0 && tiny_plan(T, E, k)) moe_tiny_kernel<0><<<1, 64, 0, s>>>(p, l);
+    else moe_small_kernel<0><<<1, kSmallWaves * 64, small_lds(E, pairs), s>>>(p, l, rows);
     return hipGetLastError();
   }
   int32_t* counts = plan + l.counts;
   const size_t lds = sizeof(int) * kSegWaves * E;
+  const size_t fused = sizeof(int) * ((kSegWaves + 2) * E + kSegWaves);
   moe_count_kernel<<<l.segments, kSegWaves * 64, lds, s>>>(ids, pairs, E, counts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (l.segments <= kPlanFusedSegments) {
+    moe_place_kernel<true><<<l.segments, kSegWaves * 64, fused, s>>>(
+        ids, pairs, E, counts, l.segments, rows, plan, plan + l.tiles, plan + l.order);
+    return hipGetLastError();
+  }
   moe_scan_kernel<<<1, 1024, sizeof(int) * (2 * E + 16), s>>>(counts, l.segments, E, rows, plan,
                                                               plan + l.tiles);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  moe_place_kernel<<<l.segments, kSegWaves * 64, lds, s>>>(ids, pairs, E, counts, plan, plan + l.order);
+  moe_place_kernel<false><<<l.segments, kSegWaves * 64, lds, s>>>(
+      ids, pairs, E, counts, l.segments, rows, plan, plan + l.tiles, plan + l.order);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_route(const RouteParams& p, hipStream_t s) {
-  const bool small = p.T <= kPlanSmallTokens && small_plan(p.E, (long long)p.T * p.k);
+  const bool small = (p.T <= kPlanSmallTokens && small_plan(p.E, (long long)p.T * p.k)) || tiny_plan(p.T, p.E, p.k);
   hipError_t e;
   if (p.E <= 64) e = route<1>(p, small, s);
   else if (p.E <= 128) e = route<2>(p, small, s);

@@ -92,6 +92,7 @@ bool moe_direct(long long pairs, int topk, int experts);
 
 // Segments the plan of many pairs is built in.
 constexpr int kPlanSegment = 2048;
+constexpr int kPlanFusedSegments = 64;  // up to here each segment sums the others' counts itself
 constexpr int kPlanSmallPairs = 1024;  // up to here one workgroup routes and plans
 constexpr int kPlanSmallTokens = 64;
 
@@ -119,6 +120,7 @@ struct RouteParams {
   const float* bias;
   int T, E, k, sigmoid, groups, top_groups, group_best, renorm;
   float scale;
+  uint32_t group_magic;  // ceil(2^20 / (E / groups))
   int32_t* ids;
   float* weights;
   int32_t* plan;  // or null

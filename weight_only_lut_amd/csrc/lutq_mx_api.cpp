@@ -93,7 +93,7 @@ constexpr int kStreamRows = 64;
 
 }  // namespace
 
-int moe_tile_rows(long long pairs, int experts) { return pairs > 16LL * experts ? 128 : 16; }
+int moe_tile_rows(long long pairs, int experts) { return pairs > 16LL * experts ? 64 : 16; }
 
 bool moe_direct(long long pairs, int topk, int experts) {
   return topk <= 16 && pairs <= 64;
@@ -265,6 +265,7 @@ int lutq_moe_route(const void* logits, int dtype, long long ld, const float* bia
   p.k = k;
   p.sigmoid = o.score == LUTQ_MOE_SIGMOID;
   p.groups = o.groups;
+  p.group_magic = ((1u << 20) + E / o.groups - 1) / (E / o.groups);
   p.top_groups = o.top_groups;
   p.group_best = o.group_best;
   p.renorm = o.renorm;

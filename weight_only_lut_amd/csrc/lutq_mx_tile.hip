@@ -17,7 +17,7 @@ typedef Mx16<DT> T;
 typedef T::frag frag;
 
 template <int MODE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxParams p, int mtiles, int ntiles) {
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, int mtiles, int ntiles) {
   constexpr bool kUp = MODE == kMxUp;
   constexpr int kThreads = WM * WN * 64;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -195,9 +195,9 @@ hipError_t go(const MxParams& p, hipStream_t s) {
 template <>
 hipError_t mx_tile<DT>(const MxParams& p, int mode, int cus, hipStream_t s) {
   switch (mode) {
-    case kMxDense: return go<kMxDense, 256, 256, 2, 4>(p, s);
-    case kMxUp: return go<kMxUp, 128, 256, 2, 4>(p, s);
-    default: return go<kMxDown, 128, 256, 2, 4>(p, s);
+    case kMxDense: return p.M <= 64 ? go<kMxDense, 64, 256, 1, 4>(p, s) : go<kMxDense, 96, 256, 1, 4>(p, s);
+    case kMxUp: return go<kMxUp, 64, 256, 1, 4>(p, s);
+    default: return go<kMxDown, 64, 256, 1, 4>(p, s);
   }
 }
 
