@@ -129,9 +129,11 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
 
 /* Bytes of workspace the two products need (device, caller-owned, 16-byte
  * aligned, free for other use once the call's work is done; may be NULL where
- * this is 0; LUTQ_ESIZE if it is smaller). four_bit: 1 for lutq_mx_matmul_mx.
- * 0 for invalid sizes. */
-size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit);
+ * this is 0; LUTQ_ESIZE if it is smaller): the results of a K split for a
+ * lutq_mx_matmul of this path (four_bit 0), the activations' scales in tile
+ * order for lutq_mx_matmul_mx (four_bit 1). Made for the current device. 0 for
+ * invalid sizes. */
+size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit, int path);
 
 #ifdef __cplusplus
 }

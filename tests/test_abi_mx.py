@@ -79,8 +79,16 @@ def test_matmul_refuses(lib):
     assert lib.lutq_mx_matmul(P, 2, 64, None, P, 1, 48, 64, 0, None, 0, None) == EINVAL
     assert m(ldx=(1 << 22) + 8) == EUNSUP
 
-    need = lib.lutq_mx_workspace_bytes(2, 48, 64, 1)
-    assert need > 0 and lib.lutq_mx_workspace_bytes(0, 48, 64, 1) == 0 == lib.lutq_mx_workspace_bytes(2, 48, 63, 1)
+    # a tall split of a small matrix keeps its results in the caller's workspace
+    split = lib.lutq_mx_workspace_bytes(96, 48, 4096, 0, 0)
+    assert split > 0 and lib.lutq_mx_workspace_bytes(96, 48, 4096, 0, 1) == 0
+    d = _desc(K=4096)
+    def ms(ws, n):
+        return lib.lutq_mx_matmul(P, 2, 4096, ctypes.addressof(d), P, 96, 48, 4096, 0, ws, n, None)
+    assert ms(None, 0) == EINVAL and ms(P, split - 1) == ESIZE and ms(P + 8, split) == EALIGN
+
+    need = lib.lutq_mx_workspace_bytes(2, 48, 64, 1, 0)
+    assert need > 0 and lib.lutq_mx_workspace_bytes(0, 48, 64, 1, 0) == 0 == lib.lutq_mx_workspace_bytes(2, 48, 63, 1, 0)
 
     def m4(xc=P, xs=P, y=P, dtype=2, M=2, N=48, K=64, ws=P, n=need, **over):
         d = _desc(**over)

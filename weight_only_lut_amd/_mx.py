@@ -49,7 +49,7 @@ def declare(lib):
             ("lutq_mx_pack", i32, [vp, vp, i32, i32, i32, vp, sz, vp, vp]),
             ("lutq_mx_matmul", i32, [vp, i32, i64, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
             ("lutq_mx_matmul_mx", i32, [vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
-            ("lutq_mx_workspace_bytes", sz, [i32, i32, i32, i32]),
+            ("lutq_mx_workspace_bytes", sz, [i32, i32, i32, i32, i32]),
             ("lutq_moe_route", i32, [vp, i32, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp]),
             ("lutq_moe_plan_ints", sz, [i32, i32, i32]),
             ("lutq_moe_plan", i32, [vp, i32, i32, i32, vp, vp]),
@@ -217,7 +217,7 @@ def mx_matmul(x, p: MxPacked, *, dtype=None, path: str = "auto", out=None):
     if out is None:
         out = _new(M, p.N, dtype, first.device)
     lib = _lib()
-    nbytes = lib.lutq_mx_workspace_bytes(M, p.N, K, four)
+    nbytes = lib.lutq_mx_workspace_bytes(M, p.N, K, four, _PATHS[path])
     space = _new(1, nbytes, torch.uint8, first.device) if nbytes else None
     at = space.data_ptr() if nbytes else None
     if four:

@@ -515,7 +515,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* pairs, co
     if ((unsigned)id >= (unsigned)E) continue;
     const float* row = pairs + ((size_t)t * k + j) * D + n;
     if ((D & 3) == 0) {
-      sum += *reinterpret_cast<const f32x4*>(row);
+      sum += __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -523,6 +523,19 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* pairs, co
     }
   }
   store4<DT>(y + (size_t)t * D, n, D, sum);
+}
+
+// y = the sum of `count` planes, in their order, rounded to 16 bits.
+template <int DT>
+__global__ __launch_bounds__(256) void mx_join_kernel(const float* parts, int count, long long plane,
+                                                       long long values, uint16_t* y) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= values) return;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(parts + i);
+#pragma unroll 4
+  for (int s = 1; s < count; ++s) sum += *reinterpret_cast<const f32x4*>(parts + s * plane + i);
+  if (i + 4 <= values) store4<DT>(y + i, 0, 4, sum);
+  else store4<DT>(y + i, 0, (int)(values - i), sum);
 }
 
 size_t small_lds(int E, int n) {
@@ -600,6 +613,15 @@ hipError_t launch_moe_route(const RouteParams& p, hipStream_t s) {
   else e = route<16>(p, small, s);
   if (e != hipSuccess || small || !p.plan) return e;
   return launch_moe_plan(p.ids, p.T, p.E, p.k, p.plan, s);
+}
+
+hipError_t launch_mx_join(const float* parts, int count, long long plane, long long values, void* y,
+                          int dtype, hipStream_t s) {
+  const unsigned g = (unsigned)((values + 1023) / 1024);
+  uint16_t* o = static_cast<uint16_t*>(y);
+  if (dtype == kF16) mx_join_kernel<kF16><<<g, 256, 0, s>>>(parts, count, plane, values, o);
+  else mx_join_kernel<kBf16><<<g, 256, 0, s>>>(parts, count, plane, values, o);
+  return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const float* pairs, const int32_t* ids, void* y, int dtype, int T,

@@ -72,7 +72,22 @@ struct MxParams {
   int max_tiles;         // entries at most (the grid)
   int pairs, topk, experts;
   void* workspace;       // the caller's, as the launcher needs it
+  // dense, by tiles: workgroups per output tile along K, and their fp32
+  // results [ksplit][plane] (in the workspace)
+  int ksplit;
 };
+
+// How a dense product runs.
+struct MxPlan {
+  int path;      // LUTQ_MX_PATH_STREAM or LUTQ_MX_PATH_TILE
+  int bm, bn;    // by tiles: the workgroup's tile
+  int ksplit;    // by tiles
+  size_t workspace;
+};
+MxPlan mx_plan(int M, int N, int K, int path, int cus);
+// The sum of a K split's results, rounded to 16 bits.
+hipError_t launch_mx_join(const float* parts, int count, long long plane, long long values, void* y,
+                          int dtype, hipStream_t s);
 
 // Bytes of M rows' scales in the tile order of packed weights.
 inline size_t mx_scale_tile_bytes(long long M, int K) {
@@ -138,16 +153,17 @@ inline hipError_t launch_mx_zero(void* y, long long n, hipStream_t s) {
 }
 // dtype: kF16 or kBf16 of x, h and y; compiled once for each.
 template <int DT> hipError_t mx_stream(const MxParams& p, int mode, int cus, hipStream_t s);
-template <int DT> hipError_t mx_tile(const MxParams& p, int mode, int cus, hipStream_t s);
+template <int DT> hipError_t mx_tile(const MxParams& p, int mode, const MxPlan& plan, hipStream_t s);
 template <> hipError_t mx_stream<kF16>(const MxParams& p, int mode, int cus, hipStream_t s);
 template <> hipError_t mx_stream<kBf16>(const MxParams& p, int mode, int cus, hipStream_t s);
-template <> hipError_t mx_tile<kF16>(const MxParams& p, int mode, int cus, hipStream_t s);
-template <> hipError_t mx_tile<kBf16>(const MxParams& p, int mode, int cus, hipStream_t s);
+template <> hipError_t mx_tile<kF16>(const MxParams& p, int mode, const MxPlan& plan, hipStream_t s);
+template <> hipError_t mx_tile<kBf16>(const MxParams& p, int mode, const MxPlan& plan, hipStream_t s);
 inline hipError_t launch_mx_stream(const MxParams& p, int dtype, int mode, int cus, hipStream_t s) {
   return dtype == kF16 ? mx_stream<kF16>(p, mode, cus, s) : mx_stream<kBf16>(p, mode, cus, s);
 }
-inline hipError_t launch_mx_tile(const MxParams& p, int dtype, int mode, int cus, hipStream_t s) {
-  return dtype == kF16 ? mx_tile<kF16>(p, mode, cus, s) : mx_tile<kBf16>(p, mode, cus, s);
+inline hipError_t launch_mx_tile(const MxParams& p, int dtype, int mode, const MxPlan& plan,
+                                 hipStream_t s) {
+  return dtype == kF16 ? mx_tile<kF16>(p, mode, plan, s) : mx_tile<kBf16>(p, mode, plan, s);
 }
 hipError_t launch_mx_tile4(const MxParams& p, int dtype, int cus, hipStream_t s);
 hipError_t launch_moe_route(const RouteParams& p, hipStream_t s);

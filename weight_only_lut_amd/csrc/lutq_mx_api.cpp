@@ -88,12 +88,58 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 // Whether a launch over row tiles x column tiles of at least 64 fits a grid.
 bool tiles_fit(long long row_tiles, long long N) { return row_tiles * ((N + 63) / 64) <= 0x7FFFFFFF; }
 
-// Rows of a stream launch above which the tiled kernel is faster.
-constexpr int kStreamRows = 64;
+// Rows up to which the stream kernel is faster than tiles (us, stream / tiles;
+// 64 rows: 14336 x 4096 17.2 / 18.8, 28672 x 8192 52 / 54; 96 rows: 28.5 / 24.3,
+// 91 / 64). On a narrow matrix with a long K its workgroups hold one weight
+// tile each and reread the activations: tiles with a K split win from 17 rows
+// (4096 x 14336: 16 rows 12.8 / 12.9, 32 rows 19.1 / 14.2, 64 rows 30.7 / 19.1).
+constexpr int kStreamRows = 64, kStreamRowsNarrow = 16;
+// Chunks of K a workgroup of a split keeps at least.
+constexpr int kSplitChunks = 4;
 
 }  // namespace
 
 int moe_tile_rows(long long pairs, int experts) { return pairs > 16LL * experts ? 64 : 16; }
+
+MxPlan mx_plan(int M, int N, int K, int path, int cus) {
+  MxPlan p = {};
+  const int nchunk = (K + kChunk - 1) / kChunk;
+  const bool narrow = N < 25 * cus && nchunk >= 64;  // 1.6 tiles of 16 per CU
+  p.path = path != LUTQ_MX_PATH_AUTO                              ? path
+           : M <= (narrow ? kStreamRowsNarrow : kStreamRows) ? LUTQ_MX_PATH_STREAM
+                                                             : LUTQ_MX_PATH_TILE;
+  p.ksplit = 1;
+  if (p.path == LUTQ_MX_PATH_STREAM) return p;
+  const auto tiles = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  // Enough tiles to fill the device: of the large shapes the one with the
+  // least work in rounds of resident workgroups, by the rates they reach on a
+  // large product (1.47, 1.42 and 1.35 PFLOP/s in bf16).
+  const struct { int bm, bn, resident; double rate; } shapes[] = {
+      {128, 512, 1, 1.0}, {128, 256, 2, 0.96}, {64, 256, 2, 0.92}};
+  double best = 0;
+  for (const auto& s : shapes) {
+    const long long t = tiles(s.bm, s.bn), slots = (long long)s.resident * cus;
+    if (t < slots) continue;
+    const double work = (double)((t + slots - 1) / slots) * s.resident * s.bm * s.bn / s.rate;
+    if (best == 0 || work < best) {
+      best = work;
+      p.bm = s.bm;
+      p.bn = s.bn;
+    }
+  }
+  if (best > 0) return p;
+  // Else smaller tiles, and K split until two workgroups per CU have work.
+  p.bm = M <= 32 ? 32 : 64;
+  p.bn = 128;
+  long long k = 2LL * cus / tiles(p.bm, p.bn);
+  if (k > nchunk / kSplitChunks) k = nchunk / kSplitChunks;
+  if (k > 1) {
+    const int per = (int)((nchunk + k - 1) / k);
+    p.ksplit = (nchunk + per - 1) / per;  // no split without a chunk
+  }
+  if (p.ksplit > 1) p.workspace = (size_t)p.ksplit * (((size_t)M * N + 3) / 4 * 4) * sizeof(float);
+  return p;
+}
 
 bool moe_direct(long long pairs, int topk, int experts) {
   return topk <= 16 && pairs <= 64;
@@ -165,9 +211,9 @@ int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N
   return LUTQ_OK;
 }
 
-size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit) {
-  if (M <= 0 || check_weights(1, N, K) || N == 0 || K == 0) return 0;
-  return four_bit ? mx_scale_tile_bytes(M, K) : 0;
+size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit, int path) {
+  if (M <= 0 || path < LUTQ_MX_PATH_AUTO || path > LUTQ_MX_PATH_TILE || check_weights(1, N, K) || N == 0 || K == 0) return 0;
+  return four_bit ? mx_scale_tile_bytes(M, K) : mx_plan(M, N, K, path, device_cu_count()).workspace;
 }
 
 int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,
@@ -188,7 +234,8 @@ int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed
   if (!x || ldx < K) return LUTQ_EINVAL;
   if (!aligned(x, 16) || ldx % 8) return LUTQ_EALIGN;
   if (ldx > kMaxLd) return LUTQ_EUNSUPPORTED;
-  rc = check_workspace(workspace, workspace_bytes, lutq_mx_workspace_bytes(M, N, K, 0));
+  const MxPlan plan = mx_plan(M, N, K, path, device_cu_count());
+  rc = check_workspace(workspace, workspace_bytes, plan.workspace);
   if (rc) return rc;
   MxParams p = {};
   p.workspace = workspace;
@@ -197,9 +244,9 @@ int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed
   p.w = weights_of(packed);
   p.y = y;
   p.M = M;
-  if (path == LUTQ_MX_PATH_AUTO) path = M <= kStreamRows ? LUTQ_MX_PATH_STREAM : LUTQ_MX_PATH_TILE;
-  return status(path == LUTQ_MX_PATH_STREAM ? launch_mx_stream(p, dtype, kMxDense, device_cu_count(), s)
-                                            : launch_mx_tile(p, dtype, kMxDense, device_cu_count(), s));
+  return status(plan.path == LUTQ_MX_PATH_STREAM
+                    ? launch_mx_stream(p, dtype, kMxDense, device_cu_count(), s)
+                    : launch_mx_tile(p, dtype, kMxDense, plan, s));
 }
 
 int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
@@ -217,7 +264,7 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
   if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
   if (!xcodes || !xscales) return LUTQ_EINVAL;
   if (!aligned(xcodes, 16)) return LUTQ_EALIGN;
-  rc = check_workspace(workspace, workspace_bytes, lutq_mx_workspace_bytes(M, N, K, 1));
+  rc = check_workspace(workspace, workspace_bytes, mx_scale_tile_bytes(M, K));
   if (rc) return rc;
   MxParams p = {};
   p.workspace = workspace;
@@ -350,9 +397,11 @@ int lutq_moe_mlp(const void* x, int dtype, long long ldx, const lutq_mx_packed_t
   }
   dn.y = out;
   const bool tiled = moe_tile_rows(pairs, E) > 16;
-  const auto product = tiled ? launch_mx_tile : launch_mx_stream;
-  e = product(up, dtype, kMxUp, cus, s);
-  if (e == hipSuccess) e = product(dn, dtype, kMxDown, cus, s);
+  const auto product = [&](const MxParams& p, int mode) {
+    return tiled ? launch_mx_tile(p, dtype, mode, MxPlan{}, s) : launch_mx_stream(p, dtype, mode, cus, s);
+  };
+  e = product(up, kMxUp);
+  if (e == hipSuccess) e = product(dn, kMxDown);
   if (e == hipSuccess) e = launch_moe_combine(out, ids, y, dtype, T, k, D, E, s);
   return status(e);
 }

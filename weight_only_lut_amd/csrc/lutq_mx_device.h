@@ -19,7 +19,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 static __device__ const u32x4 mx_zero16 = {0, 0, 0, 0};
 
 // 16 bytes per lane from memory into LDS at `dst` + 16 * lane, without passing
-// through registers; complete at the next barrier. `dst` is uniform.
+// through registers; other waves may read them after lds_ready. `dst` is uniform.
 __device__ __forceinline__ void load_to_lds(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
@@ -31,6 +31,14 @@ __device__ __forceinline__ void buffer_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_
                                               uint32_t base = 0) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, offset,
                                            base, 0, 0);
+}
+
+// A barrier behind which every wave's loads into LDS have arrived. (The barrier
+// alone does not wait for them: the compiler orders such loads with the reads
+// of the same wave only.)
+__device__ __forceinline__ void lds_ready() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
 }
 
 template <int DT> struct Mx16;
@@ -79,6 +87,21 @@ template <> struct Mx16<kBf16> {
 template <int DT>
 __device__ __forceinline__ float mx_scale(uint32_t b) {
   return __builtin_bit_cast(float, (b << 23) + ((uint32_t)Mx16<DT>::kShift << 23));
+}
+
+// Where 16-byte piece p (0 .. 15) of a 256-byte row lies in LDS: a fragment read
+// takes piece 4q + j of row r in lane 16q + r. gfx950 serves such a read in
+// groups of 16 lanes of two quarters, four neighbours of each row range (lanes
+// 0-3, 12-15, 20-23 and 24-27, and so on), so the exchange by the row must not
+// carry one quarter's pieces onto another's: the quarter's low bit toggles both
+// upper bits. (With a plain p ^ r half of the LDS cycles were bank conflicts.)
+__device__ __forceinline__ int lds_piece(int p, int row) {
+  return ((p & 3) | ((p >> 2 & 1) << 3) | (((p >> 2 ^ p >> 3) & 1) << 2)) ^ (row & 15);
+}
+// The piece that lies at slot s of a row.
+__device__ __forceinline__ int lds_piece_at(int s, int row) {
+  const int v = s ^ (row & 15);
+  return (v & 3) | ((v >> 3 & 1) << 2) | (((v >> 2 ^ v >> 3) & 1) << 3);
 }
 
 // A 16-byte load known to be from global memory (a pointer chosen at run time

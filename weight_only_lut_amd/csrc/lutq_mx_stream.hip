@@ -151,13 +151,11 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   for (int c = c0; c < c1; c += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      // piece s of row m sits at s ^ (m mod 16) of the row's sixteen: the 16
-      // rows that a fragment reads lie in different banks
 #pragma unroll
       for (int z = 0; z < PL; ++z)
 #pragma unroll
         for (int i = 0; i < RX; ++i)
-          lds.x[wave][z][(4 * i + q) * 16 + (r ^ ((4 * i + q) & 15))] = xf[u][z][i];
+          lds.x[wave][z][(4 * i + q) * 16 + lds_piece(r, 4 * i + q)] = xf[u][z][i];
       wave_lds_order();
       float s[NT];
 #pragma unroll
@@ -169,7 +167,7 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
         for (int z = 0; z < PL; ++z)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            b[z][mt] = __builtin_bit_cast(frag, lds.x[wave][z][(mt * 16 + r) * 16 + ((4 * q + j) ^ r)]);
+            b[z][mt] = __builtin_bit_cast(frag, lds.x[wave][z][(mt * 16 + r) * 16 + lds_piece(4 * q + j, r)]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const frag a = T::decode(cd[u][i][j], s[i]);

@@ -27,9 +27,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
-  const unsigned id = xcd_contiguous(blockIdx.x, gridDim.x);
-  int mt, nt;
+  unsigned id = xcd_contiguous(blockIdx.x, gridDim.x);
+  int mt, nt, c0 = 0, c1 = p.w.nchunk, split = 0;
   if constexpr (MODE == kMxDense) {
+    split = id / (mtiles * ntiles);
+    id -= split * (mtiles * ntiles);
+    const int per = (c1 + p.ksplit - 1) / p.ksplit;
+    c0 = split * per;
+    c1 = c0 + per < c1 ? c0 + per : c1;
     mt = id % mtiles;
     nt = id / mtiles;
   } else {
@@ -49,11 +54,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   const MxWeights& w = p.w;
 
   // This thread's pieces of the activations' tile: piece i is row
-  // i * kRowStep + tid / 16, column slot ^ (row & 15), the same for every i.
+  // i * kRowStep + tid / 16, and the same column for every i.
   constexpr int kRowStep = kThreads / 16;
   static_assert(kRowStep % 16 == 0, "a thread's pieces share their column");
   const int prow = threadIdx.x >> 4;
-  const int col = ((threadIdx.x & 15) ^ (prow & 15)) * 8;
+  const int col = lds_piece_at(threadIdx.x & 15, prow) * 8;
   // Rows in order go through a buffer resource, whose end makes rows past the
   // last read as zeros; gathered rows take a pointer each.
   __amdgpu_buffer_rsrc_t rs;
@@ -93,42 +98,48 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
     for (int m = 0; m < MI; ++m) acc[i][m] = f32x4{0, 0, 0, 0};
 
   // Chunk c of the activations, straight into LDS; the last chunk may end
-  // inside, where zeros come in its place.
-  auto load_x = [&](int c, u32x4* stage) {
+  // inside, where zeros come in its place. Quarter j of the loads, or all.
+  auto load_x = [&](int c, u32x4* stage, int j) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
+      if (j >= 0 && i * 4 / kLoads != j) continue;
       u32x4* dst = stage + i * kThreads + wave * kWave;
       const bool past = (c + 1) * kChunk > w.K && c * kChunk + col >= w.K;
       if constexpr (kUp) load_to_lds(past ? static_cast<const void*>(&mx_zero16) : xp[i] + (size_t)c * kChunk, dst);
       else buffer_to_lds(rs, past ? kOutOfRange : at + i * row_step + c * (kChunk * 2), dst);
     }
   };
-  auto load_w = [&](int c, u32x4* d, uint32_t* s) {
+  auto load_w = [&](int c, u32x4* d, uint32_t* s, int j) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
+      if (j >= 0 && i * 4 / NI != j) continue;
       d[i] = *reinterpret_cast<const u32x4*>(codes + ((size_t)tile[i] * w.nchunk + c) * kMxBlockBytes +
                                              lane * kMxSlotBytes);
       s[i] = scales[((size_t)tile[i] * w.nquad + c / 4) * (kWave * 4) + lane * 4 + c % 4];
     }
   };
   const int base = (wm * MI * 16 + r) * 16;
-  // One chunk: the next one's loads go out first. The barrier also waits for
-  // this chunk's activations, and for every wave to be done with the other
-  // stage.
+  // One chunk, in four steps of 32; a quarter of the next chunk's loads goes
+  // out in each, since a wave that issues them all at once waits to do so
+  // before it multiplies (the fences keep the compiler from gathering them, and
+  // from holding all steps' operands at a time: 4096 x 28672 x 8192 at 128 x 512
+  // 1.31 ms, without them 2.83). The barrier also waits for this chunk's
+  // activations, and for every wave to be done with the other stage.
   auto step = [&](int c, const u32x4* cur, u32x4* next, const u32x4* d, const uint32_t* s, u32x4* dn,
                   uint32_t* sn) {
-    __syncthreads();
+    lds_ready();
     // (without a branch, across which the compiler would move the products
     // away from their operands: past the last chunk it is fetched again)
-    const int cn = c + 1 < w.nchunk ? c + 1 : c;
-    load_x(cn, next);
-    load_w(cn, dn, sn);
+    const int cn = c + 1 < c1 ? c + 1 : c;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_x(cn, next, j);
+      load_w(cn, dn, sn, j);
       frag b[MI];
 #pragma unroll
       for (int m = 0; m < MI; ++m)
-        b[m] = __builtin_bit_cast(frag, cur[base + m * 256 + ((4 * q + j) ^ r)]);
+        b[m] = __builtin_bit_cast(frag, cur[base + m * 256 + lds_piece(4 * q + j, r)]);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const frag a = T::decode(d[i][j], mx_scale<DT>(s[i]));
@@ -139,14 +150,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   };
   u32x4 d0[NI], d1[NI];
   uint32_t s0[NI], s1[NI];
-  load_x(0, xs0);
-  load_w(0, d0, s0);
-  int c = 0;
-  for (; c + 1 < w.nchunk; c += 2) {
+  load_x(c0, xs0, -1);
+  load_w(c0, d0, s0, -1);
+  int c = c0;
+  for (; c + 1 < c1; c += 2) {
     step(c, xs0, xs1, d0, s0, d1, s1);
     step(c + 1, xs1, xs0, d1, s1, d0, s0);
   }
-  if (c < w.nchunk) step(c, xs0, xs1, d0, s0, d1, s1);
+  if (c < c1) step(c, xs0, xs1, d0, s0, d1, s1);
 
   constexpr int kOut = kUp ? NI / 2 : NI;
   const int N = kUp ? half * 16 : w.N;
@@ -171,7 +182,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
       if constexpr (MODE == kMxDown) {
         const int pair = p.order[row0 + row];
         v *= p.weights[pair];
-        store4(static_cast<float*>(p.y) + (size_t)pair * N, n, N, v);
+        // nontemporal: 400 MB of pair outputs pass by once (258 us against 365
+        // for 24570 pairs of 4096 x 1024)
+        float* out = static_cast<float*>(p.y) + (size_t)pair * N + n;
+        if ((N & 3) == 0 && n < N) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(out));
+        else if (N & 3) store4(static_cast<float*>(p.y) + (size_t)pair * N, n, N, v);
+      } else if (MODE == kMxDense && p.ksplit > 1) {
+        store4(static_cast<float*>(p.workspace) + split * p.plane + (size_t)(row0 + row) * N, n, N, v);
       } else {
         store4<DT>(static_cast<uint16_t*>(p.y) + (size_t)(row0 + row) * N, n, N, v);
       }
@@ -185,20 +202,31 @@ hipError_t go(const MxParams& p, hipStream_t s) {
   const int tiles = MODE == kMxUp ? p.w.ntile / 2 : p.w.ntile;
   const long long nt = (tiles + span - 1) / span;
   const long long mt = MODE == kMxDense ? (p.M + BM - 1) / BM : p.max_tiles;
-  if (nt * mt > 0x7FFFFFFF) return hipErrorInvalidValue;
-  mx_tile_kernel<MODE, BM, BN, WM, WN><<<dim3((unsigned)(nt * mt)), WM * WN * 64, 0, s>>>(p, (int)mt, (int)nt);
+  const int splits = MODE == kMxDense ? p.ksplit : 1;
+  if (nt * mt * splits > 0x7FFFFFFF) return hipErrorInvalidValue;
+  mx_tile_kernel<MODE, BM, BN, WM, WN>
+      <<<dim3((unsigned)(nt * mt * splits)), WM * WN * 64, 0, s>>>(p, (int)mt, (int)nt);
   return hipGetLastError();
 }
 
 }  // namespace
 
 template <>
-hipError_t mx_tile<DT>(const MxParams& p, int mode, int cus, hipStream_t s) {
-  switch (mode) {
-    case kMxDense: return p.M <= 64 ? go<kMxDense, 64, 256, 1, 4>(p, s) : go<kMxDense, 96, 256, 1, 4>(p, s);
-    case kMxUp: return go<kMxUp, 64, 256, 1, 4>(p, s);
-    default: return go<kMxDown, 64, 256, 1, 4>(p, s);
-  }
+hipError_t mx_tile<DT>(const MxParams& p, int mode, const MxPlan& plan, hipStream_t s) {
+  if (mode == kMxUp) return go<kMxUp, 64, 256, 1, 4>(p, s);
+  if (mode == kMxDown) return go<kMxDown, 64, 256, 1, 4>(p, s);
+  MxParams q = p;
+  q.ksplit = plan.ksplit;
+  q.plane = ((long long)p.M * p.w.N + 3) / 4 * 4;
+  hipError_t e;
+  if (plan.bm == 128 && plan.bn == 512) e = go<kMxDense, 128, 512, 1, 8>(q, s);
+  else if (plan.bm == 128) e = go<kMxDense, 128, 256, 1, 4>(q, s);
+  else if (plan.bm == 64 && plan.bn == 256) e = go<kMxDense, 64, 256, 1, 4>(q, s);
+  else if (plan.bm == 64) e = go<kMxDense, 64, 128, 1, 4>(q, s);
+  else e = go<kMxDense, 32, 128, 1, 4>(q, s);
+  if (e != hipSuccess || q.ksplit == 1) return e;
+  return launch_mx_join(static_cast<const float*>(q.workspace), q.ksplit, q.plane,
+                        (long long)p.M * p.w.N, p.y, DT, s);
 }
 
 }  // namespace lutq

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
   // last step the activations are out of range.)
 #define LUTQ_STEP(H, s, xs, ws, xn, wnx)                                                            \
   {                                                                                                 \
-    __syncthreads();                                                                                \
+    lds_ready();                                                                           \
     load((s) + 1, xn, wnx);                                                                         \
     _Pragma("unroll") for (int c = 0; c < 2; ++c) {                                                 \
       __builtin_amdgcn_sched_barrier(0);                                                            \
