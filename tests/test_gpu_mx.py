@@ -178,6 +178,28 @@ def test_matmul_of_two_4_bit_operands(lutq, M, N, K, dtype):
     close(y, *mx.matmul(xv, mx.dequantize(c, s)), K, dtype)
 
 
+# enough tiles to fill the device, for each of the large shapes, with ragged edges; wide
+# results whose rows are not a multiple of 16 bytes; and few tiles with a long K
+LARGE = [(2043, 8184, 160), (4220, 7928, 96), (2053, 8200, 224), (2050, 8189, 96), (4090, 4088, 288),
+         (520, 1000, 4128), (200, 130, 14336), (1030, 2056, 1056)]
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_matmul_large(lutq, M, N, K, dtype):
+    rng = np.random.default_rng(M + N + K)
+    c, s = weights(rng, N, K)
+    W, w = lutq.mx_pack(dev(c), dev(s)), mx.dequantize(c, s)
+    x = torch.from_numpy(values(rng, (M, K), 3)).to(dtype).cuda()
+    y = lutq.mx_matmul(x, W)
+    close(y, *mx.matmul(f64(x), w), K, dtype)
+    assert torch.equal(y, lutq.mx_matmul(x, W))
+    xc, xs = lutq.mx_quantize(x)
+    y = lutq.mx_matmul((xc, xs), W, dtype=dtype)
+    close(y, *mx.matmul(mx.dequantize(xc.cpu().numpy(), xs.cpu().numpy()), w), K, dtype)
+    assert torch.equal(y, lutq.mx_matmul((xc, xs), W, dtype=dtype))
+
+
 @pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("dtype", HALF)
 def test_matmul_scales_far_apart(lutq, dtype, path):

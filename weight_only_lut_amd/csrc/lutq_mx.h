@@ -72,10 +72,16 @@ struct MxParams {
   int max_tiles;         // entries at most (the grid)
   int pairs, topk, experts;
   void* workspace;       // the caller's, as the launcher needs it
-  // dense, by tiles: workgroups per output tile along K, and their fp32
-  // results [ksplit][plane] (in the workspace)
+  // by tiles: workgroups per output tile along K, and their fp32 results
+  // [ksplit][plane] (in the workspace)
   int ksplit;
+  float* parts;
 };
+
+// Bytes of M rows' scales in the tile order of packed weights.
+inline size_t mx_scale_tile_bytes(long long M, int K) {
+  return (size_t)((M + 15) / 16) * ((K + 4 * kChunk - 1) / (4 * kChunk)) * kWave * 4;
+}
 
 // How a dense product runs.
 struct MxPlan {
@@ -85,14 +91,11 @@ struct MxPlan {
   size_t workspace;
 };
 MxPlan mx_plan(int M, int N, int K, int path, int cus);
+MxPlan mx_plan4(int M, int N, int K, int cus);  // 4-bit activations
+inline long long mx_plane(long long M, long long N) { return (M * N + 3) / 4 * 4; }
 // The sum of a K split's results, rounded to 16 bits.
 hipError_t launch_mx_join(const float* parts, int count, long long plane, long long values, void* y,
                           int dtype, hipStream_t s);
-
-// Bytes of M rows' scales in the tile order of packed weights.
-inline size_t mx_scale_tile_bytes(long long M, int K) {
-  return (size_t)((M + 15) / 16) * ((K + 4 * kChunk - 1) / (4 * kChunk)) * kWave * 4;
-}
 
 // Rows of a grouped row tile, by the average number of pairs per expert:
 // what the plan cuts and the product kernels are compiled for.
@@ -165,7 +168,7 @@ inline hipError_t launch_mx_tile(const MxParams& p, int dtype, int mode, const M
                                  hipStream_t s) {
   return dtype == kF16 ? mx_tile<kF16>(p, mode, plan, s) : mx_tile<kBf16>(p, mode, plan, s);
 }
-hipError_t launch_mx_tile4(const MxParams& p, int dtype, int cus, hipStream_t s);
+hipError_t launch_mx_tile4(const MxParams& p, int dtype, const MxPlan& plan, hipStream_t s);
 hipError_t launch_moe_route(const RouteParams& p, hipStream_t s);
 hipError_t launch_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, hipStream_t s);
 hipError_t launch_moe_combine(const float* pairs, const int32_t* ids, void* y, int dtype, int T,

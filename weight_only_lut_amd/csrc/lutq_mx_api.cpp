@@ -101,6 +101,45 @@ constexpr int kSplitChunks = 4;
 
 int moe_tile_rows(long long pairs, int experts) { return pairs > 16LL * experts ? 64 : 16; }
 
+namespace {
+
+struct TileShape {
+  int bm, bn, resident;
+  double rate;
+};
+
+// The shape and K split with the least estimated time: rounds of resident
+// workgroups at the shape's rate (`macs` per CU and us at the best), 3 us for
+// a launch, and the fp32 results of a split written and read at 4 TB/s. A
+// split fills the device where there are few tiles.
+void plan_tiles(MxPlan* p, const TileShape* shapes, int count, int M, int N, int nchunk, double macs,
+                int cus) {
+  double best = 0;
+  for (int i = 0; i < count; ++i) {
+    const TileShape& s = shapes[i];
+    const long long t = (long long)((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
+    const long long slots = (long long)s.resident * cus;
+    long long most = slots / t;
+    if (most > nchunk / kSplitChunks) most = nchunk / kSplitChunks;
+    for (int split = 0; split < 2; ++split) {
+      if (split && most < 2) continue;
+      const int per = split ? (int)((nchunk + most - 1) / most) : nchunk;
+      const int k = (nchunk + per - 1) / per;  // no split without a chunk
+      const long long rounds = (t * k + slots - 1) / slots;
+      double us = 3.0 + (double)rounds * s.resident * s.bm * s.bn * per * kChunk / (macs * s.rate);
+      if (k > 1) us += 3.0 + (double)k * M * N * 8 / 4.0e6;
+      if (best == 0 || us < best) {
+        best = us;
+        p->bm = s.bm;
+        p->bn = s.bn;
+        p->ksplit = k;
+      }
+    }
+  }
+}
+
+}  // namespace
+
 MxPlan mx_plan(int M, int N, int K, int path, int cus) {
   MxPlan p = {};
   const int nchunk = (K + kChunk - 1) / kChunk;
@@ -110,34 +149,24 @@ MxPlan mx_plan(int M, int N, int K, int path, int cus) {
                                                              : LUTQ_MX_PATH_TILE;
   p.ksplit = 1;
   if (p.path == LUTQ_MX_PATH_STREAM) return p;
-  const auto tiles = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  // Enough tiles to fill the device: of the large shapes the one with the
-  // least work in rounds of resident workgroups, by the rates they reach on a
-  // large product (1.47, 1.42 and 1.35 PFLOP/s in bf16).
-  const struct { int bm, bn, resident; double rate; } shapes[] = {
-      {128, 512, 1, 1.0}, {128, 256, 2, 0.96}, {64, 256, 2, 0.92}};
-  double best = 0;
-  for (const auto& s : shapes) {
-    const long long t = tiles(s.bm, s.bn), slots = (long long)s.resident * cus;
-    if (t < slots) continue;
-    const double work = (double)((t + slots - 1) / slots) * s.resident * s.bm * s.bn / s.rate;
-    if (best == 0 || work < best) {
-      best = work;
-      p.bm = s.bm;
-      p.bn = s.bn;
-    }
-  }
-  if (best > 0) return p;
-  // Else smaller tiles, and K split until two workgroups per CU have work.
-  p.bm = M <= 32 ? 32 : 64;
-  p.bn = 128;
-  long long k = 2LL * cus / tiles(p.bm, p.bn);
-  if (k > nchunk / kSplitChunks) k = nchunk / kSplitChunks;
-  if (k > 1) {
-    const int per = (int)((nchunk + k - 1) / k);
-    p.ksplit = (nchunk + per - 1) / per;  // no split without a chunk
-  }
-  if (p.ksplit > 1) p.workspace = (size_t)p.ksplit * (((size_t)M * N + 3) / 4 * 4) * sizeof(float);
+  // Output tiles, workgroups of it resident per CU, and the share of the best
+  // rate reached by a product that fills the device (bf16, PFLOP/s: 1.49, 1.47,
+  // 1.41, 1.2, 0.8).
+  static const TileShape shapes[] = {
+      {128, 512, 1, 1.0}, {128, 256, 2, 0.98}, {64, 256, 2, 0.94}, {64, 128, 2, 0.8}, {32, 128, 2, 0.55}};
+  plan_tiles(&p, shapes, 5, M, N, nchunk, 2.9e6, cus);
+  if (p.ksplit > 1) p.workspace = (size_t)p.ksplit * mx_plane(M, N) * sizeof(float);
+  return p;
+}
+
+MxPlan mx_plan4(int M, int N, int K, int cus) {
+  MxPlan p = {};
+  p.path = LUTQ_MX_PATH_TILE;
+  // 4.1, 3.1 and 1.9 PFLOP/s; the kernel steps by four chunks
+  static const TileShape shapes[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.75}, {64, 128, 2, 0.45}};
+  plan_tiles(&p, shapes, 3, M, N, ((K + kChunk - 1) / kChunk + 3) / 4 * 4, 8.0e6, cus);
+  p.workspace = mx_scale_tile_bytes(M, K);
+  if (p.ksplit > 1) p.workspace += (size_t)p.ksplit * mx_plane(M, N) * sizeof(float);
   return p;
 }
 
@@ -213,7 +242,8 @@ int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N
 
 size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit, int path) {
   if (M <= 0 || path < LUTQ_MX_PATH_AUTO || path > LUTQ_MX_PATH_TILE || check_weights(1, N, K) || N == 0 || K == 0) return 0;
-  return four_bit ? mx_scale_tile_bytes(M, K) : mx_plan(M, N, K, path, device_cu_count()).workspace;
+  const int cus = device_cu_count();
+  return (four_bit ? mx_plan4(M, N, K, cus) : mx_plan(M, N, K, path, cus)).workspace;
 }
 
 int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,
@@ -264,7 +294,8 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
   if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
   if (!xcodes || !xscales) return LUTQ_EINVAL;
   if (!aligned(xcodes, 16)) return LUTQ_EALIGN;
-  rc = check_workspace(workspace, workspace_bytes, mx_scale_tile_bytes(M, K));
+  const MxPlan plan = mx_plan4(M, N, K, device_cu_count());
+  rc = check_workspace(workspace, workspace_bytes, plan.workspace);
   if (rc) return rc;
   MxParams p = {};
   p.workspace = workspace;
@@ -274,7 +305,7 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
   p.w = weights_of(packed);
   p.y = y;
   p.M = M;
-  return status(launch_mx_tile4(p, dtype, device_cu_count(), s));
+  return status(launch_mx_tile4(p, dtype, plan, s));
 }
 
 size_t lutq_moe_plan_ints(int T, int E, int k) {

@@ -159,41 +159,83 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   }
   if (c < c1) step(c, xs0, xs1, d0, s0, d1, s1);
 
+  // The outputs: kOut tiles of columns from n0.
   constexpr int kOut = kUp ? NI / 2 : NI;
+  constexpr bool kFloat = MODE == kMxDown;
   const int N = kUp ? half * 16 : w.N;
+  const int n0 = (nt * WN + wn) * kOut * 16;
+  f32x4 f[kOut], fu[kUp ? kOut : 1];
 #pragma unroll
   for (int i = 0; i < kOut; ++i) {
-    const int t = nt * (WN * kOut) + wn * kOut + i;
-    if (t >= limit) continue;
-    const int n = t * 16 + 4 * q;
-    const f32x4 f = row_factors(rowf, n, T::kShift);
-    f32x4 fu = f;
-    if constexpr (kUp) fu = row_factors(rowf, half * 16 + n, T::kShift);
+    f[i] = row_factors(rowf, tile[i] * 16 + 4 * q, T::kShift);
+    if constexpr (kUp) fu[i] = row_factors(rowf, tile[i + kOut] * 16 + 4 * q, T::kShift);
+  }
+  const auto value = [&](int i, int m) {
+    f32x4 v = acc[i][m] * f[i];
+    if constexpr (kUp) {
+      const f32x4 u = acc[i + kOut][m] * fu[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], u[e]);
+    }
+    return v;
+  };
+  uint16_t* y16 = static_cast<uint16_t*>(p.y);
+  float* y32 = static_cast<float*>(p.y);
+  if (MODE == kMxDense && p.ksplit > 1) {
+#pragma unroll
+    for (int i = 0; i < kOut; ++i)
+#pragma unroll
+      for (int m = 0; m < MI; ++m) {
+        const int row = (wm * MI + m) * 16 + r;
+        if (row < rows)
+          store4(p.parts + split * p.plane + (size_t)(row0 + row) * N,
+                 n0 + i * 16 + 4 * q, N, value(i, m));
+      }
+    return;
+  }
+  if (N % (kFloat ? 4 : 8) == 0) {
+    lds_ready();  // the tiles are free
+    constexpr int P = kOut * (kFloat ? 4 : 2);
+    RowStage<P> stage{xs0 + wave * (16 * P)};
+    static_assert(WM * WN * 16 * P <= BM * 16, "the waves' areas fit a stage");
 #pragma unroll
     for (int m = 0; m < MI; ++m) {
-      const int row = (wm * MI + m) * 16 + r;
-      if (row >= rows) continue;
-      f32x4 v = acc[i][m] * f;
-      if constexpr (kUp) {
-        const f32x4 u = acc[i + kOut][m] * fu;
+      const int m0 = (wm * MI + m) * 16;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], u[e]);
+      for (int i = 0; i < kOut; ++i) {
+        const f32x4 v = value(i, m);
+        if constexpr (kFloat) stage.put4(r, 4 * i + q, v);
+        else stage.put2(r, 2 * i + (q >> 1), q & 1, T::pack(v[0], v[1]), T::pack(v[2], v[3]));
       }
-      if constexpr (MODE == kMxDown) {
+      stage.drain(lane, [&](int row, int piece, u32x4 v) {
+        const int n = n0 + piece * (kFloat ? 4 : 8);
+        if (m0 + row >= rows || n >= N) return;
+        if constexpr (kFloat) {
+          // nontemporal: hundreds of MB of pair outputs pass by once (24570
+          // pairs of 4096 x 1024: 258 us against 365)
+          const int pair = p.order[row0 + m0 + row];
+          __builtin_nontemporal_store(__builtin_bit_cast(f32x4, v) * p.weights[pair],
+                                      reinterpret_cast<f32x4*>(y32 + (size_t)pair * N + n));
+        } else {
+          *reinterpret_cast<u32x4*>(y16 + (size_t)(row0 + m0 + row) * N + n) = v;
+        }
+      });
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kOut; ++i)
+#pragma unroll
+    for (int m = 0; m < MI; ++m) {
+      const int row = (wm * MI + m) * 16 + r, n = n0 + i * 16 + 4 * q;
+      if (row >= rows) continue;
+      if constexpr (kFloat) {
         const int pair = p.order[row0 + row];
-        v *= p.weights[pair];
-        // nontemporal: 400 MB of pair outputs pass by once (258 us against 365
-        // for 24570 pairs of 4096 x 1024)
-        float* out = static_cast<float*>(p.y) + (size_t)pair * N + n;
-        if ((N & 3) == 0 && n < N) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(out));
-        else if (N & 3) store4(static_cast<float*>(p.y) + (size_t)pair * N, n, N, v);
-      } else if (MODE == kMxDense && p.ksplit > 1) {
-        store4(static_cast<float*>(p.workspace) + split * p.plane + (size_t)(row0 + row) * N, n, N, v);
+        store4(y32 + (size_t)pair * N, n, N, value(i, m) * p.weights[pair]);
       } else {
-        store4<DT>(static_cast<uint16_t*>(p.y) + (size_t)(row0 + row) * N, n, N, v);
+        store4<DT>(y16 + (size_t)(row0 + row) * N, n, N, value(i, m));
       }
     }
-  }
 }
 
 template <int MODE, int BM, int BN, int WM, int WN>
@@ -217,7 +259,8 @@ hipError_t mx_tile<DT>(const MxParams& p, int mode, const MxPlan& plan, hipStrea
   if (mode == kMxDown) return go<kMxDown, 64, 256, 1, 4>(p, s);
   MxParams q = p;
   q.ksplit = plan.ksplit;
-  q.plane = ((long long)p.M * p.w.N + 3) / 4 * 4;
+  q.parts = static_cast<float*>(p.workspace);
+  q.plane = mx_plane(p.M, p.w.N);
   hipError_t e;
   if (plan.bm == 128 && plan.bn == 512) e = go<kMxDense, 128, 512, 1, 8>(q, s);
   else if (plan.bm == 128) e = go<kMxDense, 128, 256, 1, 4>(q, s);
@@ -225,7 +268,7 @@ hipError_t mx_tile<DT>(const MxParams& p, int mode, const MxPlan& plan, hipStrea
   else if (plan.bm == 64) e = go<kMxDense, 64, 128, 1, 4>(q, s);
   else e = go<kMxDense, 32, 128, 1, 4>(q, s);
   if (e != hipSuccess || q.ksplit == 1) return e;
-  return launch_mx_join(static_cast<const float*>(q.workspace), q.ksplit, q.plane,
+  return launch_mx_join(q.parts, q.ksplit, q.plane,
                         (long long)p.M * p.w.N, p.y, DT, s);
 }
 

@@ -20,7 +20,7 @@ __device__ __forceinline__ i32x8 widen(u32x4 v) {
 }
 
 template <int DT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, int mtiles) {
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, int mtiles, int ntiles) {
   constexpr int kWaves = WM * WN;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr int XL = BM / 8 / kWaves, WL = BN / 8 / kWaves;  // KiB per wave and step
@@ -30,7 +30,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
-  const unsigned id = xcd_contiguous(blockIdx.x, gridDim.x);
+  unsigned id = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int split = (int)(id / (mtiles * ntiles));
+  id -= split * (mtiles * ntiles);
   const int row0 = (int)(id % mtiles) * BM, nt = (int)(id / mtiles);
   const int rows = p.M - row0 < BM ? p.M - row0 : BM;
   const MxWeights& w = p.w;
@@ -106,6 +108,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
   {                                                                                                 \
     lds_ready();                                                                           \
     load((s) + 1, xn, wnx);                                                                         \
+    if (H == 0) load_scales((s) / 2 + 1, sxn, swn);                                                 \
     _Pragma("unroll") for (int c = 0; c < 2; ++c) {                                                 \
       __builtin_amdgcn_sched_barrier(0);                                                            \
       i32x8 b[MI];                                                                                  \
@@ -125,10 +128,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
     }                                                                                               \
     __builtin_amdgcn_sched_barrier(0);                                                              \
   }
-  load(0, xs0, ws0);
-  load_scales(0, sx, sw);
-  for (int quad = 0; quad < w.nquad; ++quad) {
-    load_scales(quad + 1, sxn, swn);
+  const int per = (w.nquad + p.ksplit - 1) / p.ksplit, quad0 = split * per;
+  const int quad1 = quad0 + per < w.nquad ? quad0 + per : w.nquad;
+  load(2 * quad0, xs0, ws0);
+  load_scales(quad0, sx, sw);
+  for (int quad = quad0; quad < quad1; ++quad) {
     LUTQ_STEP(0, 2 * quad, xs0, ws0, xs1, ws1)
     LUTQ_STEP(1, 2 * quad + 1, xs1, ws1, xs0, ws0)
 #pragma unroll
@@ -138,19 +142,54 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
   }
 #undef LUTQ_STEP
 
+  uint16_t* y = static_cast<uint16_t*>(p.y);
+  const int n0 = (nt * (BN / 16) + wn * NI) * 16;
+  f32x4 f[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int t = nt * (BN / 16) + wn * NI + i;
-    if (t >= w.ntile) continue;
-    const int n = t * 16 + 4 * q;
-    const f32x4 f = row_factors(w.rows, n, 0);
+    const int t = n0 / 16 + i;
+    f[i] = row_factors(w.rows, (t < w.ntile ? t : w.ntile - 1) * 16 + 4 * q, 0);
+  }
+  if (p.ksplit > 1) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int m = 0; m < MI; ++m) {
+        const int row = (wm * MI + m) * 16 + r;
+        if (row < rows)
+          store4(p.parts + split * p.plane + (size_t)(row0 + row) * w.N, n0 + i * 16 + 4 * q, w.N,
+                 acc[i][m] * f[i]);
+      }
+    return;
+  }
+  if (w.N % 8 == 0) {
+    lds_ready();  // the tiles are free
+    constexpr int P = NI * 2;
+    RowStage<P> stage{ws0 + wave * (16 * P)};
+    static_assert(kWaves * 16 * P <= BN * 8, "the waves' areas fit a stage of the weights");
 #pragma unroll
     for (int m = 0; m < MI; ++m) {
-      const int row = row0 + (wm * MI + m) * 16 + r;
-      if (row < p.M)
-        store4<DT>(static_cast<uint16_t*>(p.y) + (size_t)row * w.N, n, w.N, acc[i][m] * f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const f32x4 v = acc[i][m] * f[i];
+        stage.put2(r, 2 * i + (q >> 1), q & 1, Mx16<DT>::pack(v[0], v[1]), Mx16<DT>::pack(v[2], v[3]));
+      }
+      const int m0 = (wm * MI + m) * 16;
+      stage.drain(lane, [&](int row, int piece, u32x4 v) {
+        const int n = n0 + piece * 8;
+        if (m0 + row < rows && n < w.N)
+          *reinterpret_cast<u32x4*>(y + (size_t)(row0 + m0 + row) * w.N + n) = v;
+      });
     }
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int m = 0; m < MI; ++m) {
+      const int row = (wm * MI + m) * 16 + r;
+      if (row < rows) store4<DT>(y + (size_t)(row0 + row) * w.N, n0 + i * 16 + 4 * q, w.N, acc[i][m] * f[i]);
+    }
 }
 
 // The activations' scale bytes [M][K/32] in the order of the packed weights'
@@ -179,29 +218,36 @@ __global__ __launch_bounds__(256) void mx_scale_tiles_kernel(const uint8_t* scal
 template <int DT, int BM, int BN, int WM, int WN>
 hipError_t go(const MxParams& p, hipStream_t s) {
   const long long mt = (p.M + BM - 1) / BM, nt = (p.w.ntile + BN / 16 - 1) / (BN / 16);
-  if (mt * nt > 0x7FFFFFFF) return hipErrorInvalidValue;
-  mx_tile4_kernel<DT, BM, BN, WM, WN><<<dim3((unsigned)(mt * nt)), WM * WN * 64, 0, s>>>(p, (int)mt);
+  if (mt * nt * p.ksplit > 0x7FFFFFFF) return hipErrorInvalidValue;
+  mx_tile4_kernel<DT, BM, BN, WM, WN>
+      <<<dim3((unsigned)(mt * nt * p.ksplit)), WM * WN * 64, 0, s>>>(p, (int)mt, (int)nt);
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t pick(const MxParams& p, int cus, hipStream_t s) {
-  if (p.M <= 64) return go<DT, 64, 128, 2, 4>(p, s);
-  return go<DT, 256, 256, 4, 2>(p, s);
+hipError_t pick(const MxParams& p, const MxPlan& plan, hipStream_t s) {
+  if (plan.bm == 256) return go<DT, 256, 256, 2, 4>(p, s);
+  if (plan.bm == 128) return go<DT, 128, 128, 2, 2>(p, s);
+  return go<DT, 64, 128, 2, 4>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_mx_tile4(const MxParams& p, int dtype, int cus, hipStream_t s) {
-  const int nquad = p.w.nquad;
+hipError_t launch_mx_tile4(const MxParams& p, int dtype, const MxPlan& plan, hipStream_t s) {
   const long long n = (long long)mx_scale_tile_bytes(p.M, p.w.K) / 4;
-  mx_scale_tiles_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
-      p.xscales, p.M, p.w.K / kMxBlock, nquad, static_cast<uint32_t*>(p.workspace));
-  const hipError_t e = hipGetLastError();
+  uint32_t* scales = static_cast<uint32_t*>(p.workspace);
+  mx_scale_tiles_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p.xscales, p.M, p.w.K / kMxBlock,
+                                                                    p.w.nquad, scales);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   MxParams q = p;
-  q.xscales = static_cast<const uint8_t*>(p.workspace);
-  return dtype == kF16 ? pick<kF16>(q, cus, s) : pick<kBf16>(q, cus, s);
+  q.xscales = reinterpret_cast<const uint8_t*>(scales);
+  q.parts = reinterpret_cast<float*>(scales + n);
+  q.ksplit = plan.ksplit;
+  q.plane = mx_plane(p.M, p.w.N);
+  e = dtype == kF16 ? pick<kF16>(q, plan, s) : pick<kBf16>(q, plan, s);
+  if (e != hipSuccess || q.ksplit == 1) return e;
+  return launch_mx_join(q.parts, q.ksplit, q.plane, (long long)p.M * p.w.N, p.y, dtype, s);
 }
 
 }  // namespace lutq
