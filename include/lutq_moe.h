@@ -77,8 +77,8 @@ int lutq_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* plan, void* 
  *   x       : device, fp16 or bf16 [T][D], row stride ldx, as lutq_mx_matmul.
  *   y       : device, [T][D] contiguous in `dtype`, 8-byte aligned.
  *   workspace : device, lutq_moe_workspace_bytes(T, k, D, F), 16-byte aligned.
- * Sums are fp32; silu(g) * u is rounded to `dtype` in calls of many pairs and
- * keeps 16 bits of significand in calls of few; each expert's output stays
+ * Sums are fp32; silu(g) * u is rounded to `dtype` (in calls of a
+ * few pairs, 16 at most, it keeps 16 bits of significand); each expert's output stays
  * fp32 until the weighted sum, which runs in the order of j and is rounded
  * once. No atomics: results repeat bit for bit.
  * Errors: LUTQ_EINVAL, LUTQ_EMISMATCH (the descriptors do not fit each other),

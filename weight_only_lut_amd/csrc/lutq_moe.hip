@@ -7,8 +7,9 @@
 // choice is a wave maximum over the lanes' first keys (four DPP steps, then
 // scalar code) and a ballot for the lowest lane that has it.
 //
-// The plan is a stable counting sort. Up to 64 pairs a single wave plans by
-// comparing every pair with every other, up to 1024 one workgroup sorts, both
+// The plan is a stable counting sort. For the few pairs whose products need no
+// row tiles a single wave plans by comparing every pair with every other, up
+// to 1024 pairs one workgroup sorts, both
 // in the launch that routes, since there the launches are the time. Beyond
 // that, segments of 2048 pairs are counted, and each segment places its pairs
 // behind those of earlier ones. Ranks come from ballots, never from the order
@@ -323,16 +324,15 @@ __device__ void count_pairs(int* run, int E, int b, int n, Id id_of) {
   __syncthreads();
 }
 
-// At most 64 pairs: a wave per token routes (unless VPT is 0), then the first
-// wave finds each pair's position by counting the pairs before it. No row
-// tiles: the products of so few pairs do not use them.
-constexpr int kTinyPairs = kWave;
-constexpr int kTinyWaves = 16;
+// Few pairs: a wave per token routes (unless VPT is 0), then the first wave
+// finds each pair's position by counting the pairs before it. No row tiles:
+// the products of so few pairs do not use them.
+constexpr int kTinyWaves = kDirectPairs;
 
 template <int VPT>
 __global__ __launch_bounds__(kTinyWaves * 64) void moe_tiny_kernel(RouteParams p, MoePlanLayout l) {
   __shared__ float keys[kTinyWaves][VPT > 0 ? VPT * kWave : 1];
-  __shared__ int32_t ids[kTinyPairs];
+  __shared__ int32_t ids[kDirectPairs];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = p.T * p.k, waves = blockDim.x >> 6;
   if constexpr (VPT > 0) {
@@ -548,15 +548,12 @@ bool small_plan(int E, long long pairs) {
 }
 
 // The same for one wave: the products then run without row tiles.
-bool tiny_plan(int T, int E, int k) {
-  return (long long)T * k <= kTinyPairs && moe_direct((long long)T * k, k, E);
-}
+bool tiny_plan(int T, int E, int k) { return T > 0 && moe_direct((long long)T * k, k, E); }
 
 template <int VPT>
 hipError_t route(const RouteParams& p, bool small, hipStream_t s) {
   if (tiny_plan(p.T, p.E, p.k)) {
-    const int waves = p.T < kTinyWaves ? p.T : kTinyWaves;
-    moe_tiny_kernel<VPT><<<1, waves * 64, 0, s>>>(p, moe_plan_layout(p.T, p.E, p.k));
+    moe_tiny_kernel<VPT><<<1, p.T * 64, 0, s>>>(p, moe_plan_layout(p.T, p.E, p.k));
   } else if (small) {
     const MoePlanLayout l = moe_plan_layout(p.T, p.E, p.k);
     moe_small_kernel<VPT><<<1, kSmallWaves * 64, small_lds(p.E, p.T * p.k), s>>>(
@@ -579,7 +576,7 @@ hipError_t launch_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* pla
     p.k = k;
     p.ids = const_cast<int32_t*>(ids);
     p.plan = plan;
-    if (pairs > 0 && tiny_plan(T, E, k)) moe_tiny_kernel<0><<<1, 64, 0, s>>>(p, l);
+    if (tiny_plan(T, E, k)) moe_tiny_kernel<0><<<1, 64, 0, s>>>(p, l);
     else moe_small_kernel<0><<<1, kSmallWaves * 64, small_lds(E, pairs), s>>>(p, l, rows);
     return hipGetLastError();
   }

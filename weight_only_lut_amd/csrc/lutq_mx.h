@@ -49,8 +49,10 @@ struct MxWeights {
 // What a product kernel does with rows: see lutq_mx_matmul.hip.
 enum MxMode {
   kMxDense = 0,     // row m of x -> row m of y
+  // by tiles
   kMxUp = 1,        // experts' gate and up rows: sorted pair p reads x[order[p] / k], writes h[p]
   kMxDown = 2,      // experts' down rows: h[p] -> fp32 pair output order[p], times its weight
+  // streamed
   kMxUpPair = 3,    // as kMxUp for pair p itself (no order), one pair per workgroup
   kMxDownToken = 4  // all pairs of a token: h[t * k + j] -> y[t]
 };
@@ -60,8 +62,8 @@ struct MxParams {
   const uint8_t* xscales;
   long long ldx;         // elements (bytes for 4-bit codes)
   MxWeights w;
-  void* y;               // dense: 16-bit [M][N]; up: h [pairs][F], two bf16 planes (stream) or
-                         // 16-bit (tile); down: fp32 [pairs][D]; down-token: 16-bit [T][D]
+  void* y;               // dense: 16-bit [M][N]; up: h [pairs][F]; up-pair: h as two bf16 planes;
+                         // down: fp32 [pairs][D]; down-token: 16-bit [T][D]
   long long plane;       // elements between the planes of h
   int M;                 // dense: rows
   // grouped
@@ -105,7 +107,8 @@ inline long long moe_max_tiles(long long pairs, int experts, int rows) {
   const long long e = experts < pairs ? experts : pairs;
   return pairs / rows + e;
 }
-// The pairs up to which the experts' products run pair by pair, without a plan.
+// Whether the experts' products run pair by pair, without a plan.
+constexpr int kDirectPairs = 16;  // at most
 bool moe_direct(long long pairs, int topk, int experts);
 
 // Segments the plan of many pairs is built in.

@@ -99,7 +99,13 @@ constexpr int kSplitChunks = 4;
 
 }  // namespace
 
-int moe_tile_rows(long long pairs, int experts) { return pairs > 16LL * experts ? 64 : 16; }
+// us of both products of 64 experts of 4096 x 1024, 6 per token, with row tiles
+// of 16 / 32 / 64 (the better of 128 and 256 columns): 3 pairs per expert
+// 57 / 61 / 82, 12 81 / 83 / 94, 24 96 / 91 / 119, 48 147 / 121 / 143,
+// 384 836 / 602 / 560.
+int moe_tile_rows(long long pairs, int experts) {
+  return pairs <= 12LL * experts ? 16 : pairs <= 96LL * experts ? 32 : 64;
+}
 
 namespace {
 
@@ -170,8 +176,12 @@ MxPlan mx_plan4(int M, int N, int K, int cus) {
   return p;
 }
 
+// Pair by pair, an expert's weights are read once per pair: best while few
+// pairs share an expert (us, pairs / tiles; 64 experts as above: 12 pairs
+// 29 / 35, 48 87 / 53; 32 experts of 2048 x 1024: 16 pairs 25 / 25, 32 42 / 26;
+// 8 experts of 4096 x 1024: 8 pairs 23 / 28, 16 39 / 31).
 bool moe_direct(long long pairs, int topk, int experts) {
-  return topk <= 16 && pairs <= 64;
+  return topk <= 16 && pairs <= kDirectPairs && 2 * pairs <= 3LL * experts;
 }
 
 }  // namespace lutq
@@ -427,12 +437,17 @@ int lutq_moe_mlp(const void* x, int dtype, long long ldx, const lutq_mx_packed_t
     return status(launch_mx_stream(dn, dtype, kMxDownToken, cus, s));
   }
   dn.y = out;
-  const bool tiled = moe_tile_rows(pairs, E) > 16;
-  const auto product = [&](const MxParams& p, int mode) {
-    return tiled ? launch_mx_tile(p, dtype, mode, MxPlan{}, s) : launch_mx_stream(p, dtype, mode, cus, s);
+  // Narrower tiles where the wider leave the device short of workgroups.
+  MxPlan tile = {};
+  tile.bm = moe_tile_rows(pairs, E);
+  const auto columns = [&](int N) {
+    const long long wide = (long long)l.max_tiles * ((N + 255) / 256);
+    return tile.bm == 16 || wide < (tile.bm == 32 ? 2LL : 5LL) * cus ? 128 : 256;
   };
-  e = product(up, kMxUp);
-  if (e == hipSuccess) e = product(dn, kMxDown);
+  tile.bn = columns(2 * F);
+  e = launch_mx_tile(up, dtype, kMxUp, tile, s);
+  tile.bn = columns(D);
+  if (e == hipSuccess) e = launch_mx_tile(dn, dtype, kMxDown, tile, s);
   if (e == hipSuccess) e = launch_moe_combine(out, ids, y, dtype, T, k, D, E, s);
   return status(e);
 }

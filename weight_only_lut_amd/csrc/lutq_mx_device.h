@@ -104,11 +104,6 @@ __device__ __forceinline__ int lds_piece_at(int s, int row) {
   return (v & 3) | ((v >> 3 & 1) << 2) | (((v >> 2 ^ v >> 3) & 1) << 3);
 }
 
-// A 16-byte load known to be from global memory (a pointer chosen at run time
-// otherwise becomes a generic access, which also counts as an LDS access).
-__device__ __forceinline__ u32x4 global16(const void* p) {
-  return *(const __attribute__((address_space(1))) u32x4*)p;
-}
 __device__ __forceinline__ u32x4 buffer16(__amdgpu_buffer_rsrc_t rs, uint32_t offset) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, offset, 0, 0));
 }
@@ -192,9 +187,9 @@ template <int P> struct RowStage {
   template <class Out> __device__ __forceinline__ void drain(int lane, Out out) {
     wave_lds_order();
 #pragma unroll
-    for (int t = 0; t < 16 * P / kWave; ++t) {
+    for (int t = 0; t < (16 * P + kWave - 1) / kWave; ++t) {
       const int i = t * kWave + lane, row = i / P, p = i % P;
-      out(row, p, area[slot(row, p)]);
+      if (16 * P % kWave == 0 || i < 16 * P) out(row, p, area[slot(row, p)]);
     }
     wave_lds_order();
   }

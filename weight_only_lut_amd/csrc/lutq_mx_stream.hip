@@ -15,13 +15,12 @@
 // different rows, get 16 bytes per clock and CU: 30 us instead of 8 at 32
 // rows of 4096 x 14336.)
 //
-// The experts' modes keep h = silu(g) * u as two bf16 planes, the value and
-// what its rounding left, at no cost where bytes bound the products: of the
-// operator's roundings only the last remains, and h has the range of fp32
-// also in fp16 models.
+// For few (token, expert) pairs the experts' products run here pair by pair:
+// up-pair, then all of a token's down products in one workgroup. They keep
+// h = silu(g) * u as two bf16 planes, the value and what its rounding left, at
+// no cost where bytes bound the products: of the operator's roundings only the
+// last remains, and h has the range of fp32 also in fp16 models.
 // Compiled once per activation type (LUTQ_MX_TYPE).
-#include <type_traits>
-
 #include "lutq_mx_device.h"
 
 namespace lutq {
@@ -29,7 +28,7 @@ namespace {
 
 constexpr int DT = LUTQ_MX_TYPE;
 
-// Eight bf16 planes of h: 4 values n .. n + 3 of a row, hi and lo `plane` apart.
+// Four values of a row of h as bf16, and `plane` elements on what that left.
 __device__ __forceinline__ void store_h(uint16_t* row, size_t plane, const f32x4& v) {
   f32x4 hi, lo;
 #pragma unroll
@@ -42,20 +41,18 @@ __device__ __forceinline__ void store_h(uint16_t* row, size_t plane, const f32x4
       u32x2{Mx16<kBf16>::pack(lo[0], lo[1]), Mx16<kBf16>::pack(lo[2], lo[3])};
 }
 
-// MODE (see MxMode): dense, up, down and up-pair. For the up modes half of
-// the NT tiles are gate rows and half the up rows that meet them. W waves;
-// RX loads of 4 rows cover the rows (16 * MT of them at most); U chunks are
-// in flight per wave.
+// MODE (see MxMode): dense or up-pair. For up-pair half of the NT tiles are
+// gate rows and half the up rows that meet them. W waves; RX loads of 4 rows
+// cover the rows (16 * MT of them at most); U chunks are in flight per wave.
 template <int MODE, int W, int NT, int RX, int U>
 __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
-  constexpr bool kUp = MODE == kMxUp || MODE == kMxUpPair;
-  constexpr bool kDown = MODE == kMxDown;  // x is h
-  constexpr int MT = (RX + 3) / 4, PL = kDown ? 2 : 1;
-  typedef Mx16<kDown ? kBf16 : DT> T;
-  typedef typename T::frag frag;
+  constexpr bool kUp = MODE == kMxUpPair;
+  constexpr int MT = (RX + 3) / 4;
+  typedef Mx16<DT> T;
+  typedef T::frag frag;
   // the waves' activations, then their sums
   __shared__ union {
-    u32x4 x[W][PL][MT * 256];
+    u32x4 x[W][MT * 256];
     f32x4 red[W][NT * MT][kWave];
   } lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -64,41 +61,24 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   if constexpr (MODE == kMxDense) {
     row0 = blockIdx.y * 16 * MT;
     rows = p.M - row0 < 16 * MT ? p.M - row0 : 16 * MT;
-  } else if constexpr (MODE == kMxUpPair) {
+  } else {
     row0 = blockIdx.y;
     rows = 1;
     expert = p.ids[row0];
     if ((unsigned)expert >= (unsigned)p.experts) return;
-  } else {
-    if ((int)blockIdx.y >= p.tiles[0]) return;
-    const int32_t* t = p.tiles + 4 + 4 * blockIdx.y;
-    expert = t[0];
-    row0 = t[1];
-    rows = t[2];
   }
   const MxWeights& w = p.w;
   const float* rowf = w.rows + expert * w.expert_rows;
-  // Load i of a chunk is rows 4i + q, 16 bytes per lane. Rows in order (dense,
-  // h) lie behind a buffer resource, gathered rows are pointers. Rows past
-  // the last read the last: their columns are not stored.
-  constexpr bool kGather = MODE == kMxUp;
-  __amdgpu_buffer_rsrc_t xrs[PL];
+  // Load i of a chunk is rows 4i + q, 16 bytes per lane, behind a buffer
+  // resource. Rows past the last read the last: their columns are not stored.
+  const __amdgpu_buffer_rsrc_t xrs =
+      make_rsrc(static_cast<const uint16_t*>(p.x) + (long long)(kUp ? row0 / p.topk : row0) * p.ldx,
+                (uint32_t)(((rows - 1) * p.ldx + w.K) * 2));
   uint32_t xoff[RX];
-  const uint16_t* xp[kGather ? RX : 1];
-  {
-    const long long first = MODE == kMxUpPair ? row0 / p.topk : kGather ? 0 : row0;
-    const uint16_t* base = static_cast<const uint16_t*>(p.x) + first * p.ldx;
-    if constexpr (!kGather) {
 #pragma unroll
-      for (int z = 0; z < PL; ++z)
-        xrs[z] = make_rsrc(base + z * p.plane, (uint32_t)(((rows - 1) * p.ldx + w.K) * 2));
-    }
-#pragma unroll
-    for (int i = 0; i < RX; ++i) {
-      const int m = 4 * i + q, in = m < rows ? m : rows - 1;
-      if constexpr (kGather) xp[i] = base + (long long)(p.order[row0 + in] / p.topk) * p.ldx + 8 * r;
-      else xoff[i] = (uint32_t)((in * p.ldx + 8 * r) * 2);
-    }
+  for (int i = 0; i < RX; ++i) {
+    const int m = 4 * i + q, in = m < rows ? m : rows - 1;
+    xoff[i] = (uint32_t)((in * p.ldx + 8 * r) * 2);
   }
   TileBuffers tile[NT];
   const int half = w.ntile / 2;  // up modes: F / 16
@@ -124,7 +104,7 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   // U chunks in flight: each slot is refilled as soon as it is used. Loads
   // past the wave's last chunk are out of range, so they touch no memory and
   // every path has the same loads outstanding.
-  u32x4 cd[U][NT], xf[U][PL][RX];
+  u32x4 cd[U][NT], xf[U][RX];
   uint32_t sc[U][NT];
   auto load = [&](int u, int c) {
     const bool in = c < c1;
@@ -136,15 +116,8 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
     }
     const bool valid = in && c * kChunk + 8 * r < w.K;
 #pragma unroll
-    for (int i = 0; i < RX; ++i) {
-      if constexpr (kGather) {
-        xf[u][0][i] = global16(valid ? static_cast<const void*>(xp[i] + (size_t)c * kChunk) : &mx_zero16);
-      } else {
-#pragma unroll
-        for (int z = 0; z < PL; ++z)
-          xf[u][z][i] = buffer16(xrs[z], valid ? xoff[i] + (uint32_t)c * (kChunk * 2) : kOutOfRange);
-      }
-    }
+    for (int i = 0; i < RX; ++i)
+      xf[u][i] = buffer16(xrs, valid ? xoff[i] + (uint32_t)c * (kChunk * 2) : kOutOfRange);
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u, c0 + u);
@@ -152,29 +125,22 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int z = 0; z < PL; ++z)
-#pragma unroll
-        for (int i = 0; i < RX; ++i)
-          lds.x[wave][z][(4 * i + q) * 16 + lds_piece(r, 4 * i + q)] = xf[u][z][i];
+      for (int i = 0; i < RX; ++i) lds.x[wave][(4 * i + q) * 16 + lds_piece(r, 4 * i + q)] = xf[u][i];
       wave_lds_order();
       float s[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) s[i] = mx_scale<T::kType>(sc[u][i]);
+      for (int i = 0; i < NT; ++i) s[i] = mx_scale<DT>(sc[u][i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        frag b[PL][MT];
+        frag b[MT];
 #pragma unroll
-        for (int z = 0; z < PL; ++z)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            b[z][mt] = __builtin_bit_cast(frag, lds.x[wave][z][(mt * 16 + r) * 16 + lds_piece(4 * q + j, r)]);
+        for (int mt = 0; mt < MT; ++mt)
+          b[mt] = __builtin_bit_cast(frag, lds.x[wave][(mt * 16 + r) * 16 + lds_piece(4 * q + j, r)]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const frag a = T::decode(cd[u][i][j], s[i]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int z = PL - 1; z >= 0; --z) acc[i][mt] = T::mfma(a, b[z][mt], acc[i][mt]);
+          for (int mt = 0; mt < MT; ++mt) acc[i][mt] = T::mfma(a, b[mt], acc[i][mt]);
         }
       }
       wave_lds_order();
@@ -209,10 +175,6 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], u[e]);
       store_h(static_cast<uint16_t*>(p.y) + (size_t)(row0 + m) * (half * 16) + n, p.plane, v);
-    } else if constexpr (MODE == kMxDown) {
-      const int pair = p.order[row0 + m];
-      v *= p.weights[pair];
-      store4(static_cast<float*>(p.y) + (size_t)pair * w.N, n, w.N, v);
     } else {
       store4<DT>(static_cast<uint16_t*>(p.y) + (size_t)(row0 + m) * w.N, n, w.N, v);
     }
@@ -317,7 +279,7 @@ __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
 
 template <int MODE, int W, int NT, int RX, int U>
 hipError_t go(const MxParams& p, hipStream_t s) {
-  constexpr bool kUp = MODE == kMxUp || MODE == kMxUpPair;
+  constexpr bool kUp = MODE == kMxUpPair;
   constexpr int kRows = (RX + 3) / 4 * 16;
   const int tiles = kUp ? p.w.ntile / 2 : p.w.ntile, per = kUp ? NT / 2 : NT;
   const unsigned gx = (unsigned)((tiles + per - 1) / per);
@@ -335,8 +297,7 @@ hipError_t go(const MxParams& p, hipStream_t s) {
     }
     return hipSuccess;
   } else {
-    const unsigned gy = MODE == kMxUpPair ? (unsigned)p.pairs : (unsigned)p.max_tiles;
-    mx_stream_kernel<MODE, W, NT, RX, U><<<dim3(gx, gy), W * 64, 0, s>>>(q);
+    mx_stream_kernel<MODE, W, NT, RX, U><<<dim3(gx, (unsigned)p.pairs), W * 64, 0, s>>>(q);
     return hipGetLastError();
   }
 }
@@ -374,8 +335,6 @@ template <>
 hipError_t mx_stream<DT>(const MxParams& p, int mode, int cus, hipStream_t s) {
   switch (mode) {
     case kMxDense: return dense(p, cus, s);
-    case kMxUp: return go<kMxUp, 8, 2, 4, 4>(p, s);
-    case kMxDown: return go<kMxDown, 8, 1, 4, 2>(p, s);
     case kMxUpPair: return go<kMxUpPair, 8, 2, 1, 4>(p, s);
     default: {
       mx_down_token_kernel<8, 1, 4><<<dim3((unsigned)p.w.ntile, (unsigned)p.M), 512, 0, s>>>(p);

@@ -27,7 +27,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
-  unsigned id = xcd_contiguous(blockIdx.x, gridDim.x);
+  // the grid has room for the most row tiles there can be; those there are
+  // spread evenly over the XCDs
+  const unsigned total = MODE == kMxDense ? gridDim.x : (unsigned)(p.tiles[0] * ntiles);
+  if (blockIdx.x >= total) return;
+  unsigned id = xcd_contiguous(blockIdx.x, total);
   int mt, nt, c0 = 0, c1 = p.w.nchunk, split = 0;
   if constexpr (MODE == kMxDense) {
     split = id / (mtiles * ntiles);
@@ -45,7 +49,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   if constexpr (MODE == kMxDense) {
     rows = p.M - row0 < BM ? p.M - row0 : BM;
   } else {
-    if (mt >= p.tiles[0]) return;
     const int32_t* t = p.tiles + 4 + 4 * mt;
     expert = t[0];
     row0 = t[1];
@@ -196,8 +199,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   if (N % (kFloat ? 4 : 8) == 0) {
     lds_ready();  // the tiles are free
     constexpr int P = kOut * (kFloat ? 4 : 2);
-    RowStage<P> stage{xs0 + wave * (16 * P)};
-    static_assert(WM * WN * 16 * P <= BM * 16, "the waves' areas fit a stage");
+    constexpr int kArea = WM * WN * 16 * P;
+    __shared__ u32x4 own[kArea > BM * 16 ? kArea : 1];
+    RowStage<P> stage{(kArea > BM * 16 ? own : xs0) + wave * (16 * P)};
 #pragma unroll
     for (int m = 0; m < MI; ++m) {
       const int m0 = (wm * MI + m) * 16;
@@ -251,12 +255,19 @@ hipError_t go(const MxParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int MODE>
+hipError_t grouped(const MxParams& p, const MxPlan& plan, hipStream_t s) {
+  if (plan.bm == 16) return go<MODE, 16, 128, 1, 4>(p, s);
+  if (plan.bm == 32) return plan.bn == 128 ? go<MODE, 32, 128, 1, 4>(p, s) : go<MODE, 32, 256, 1, 4>(p, s);
+  return plan.bn == 128 ? go<MODE, 64, 128, 1, 4>(p, s) : go<MODE, 64, 256, 1, 4>(p, s);
+}
+
 }  // namespace
 
 template <>
 hipError_t mx_tile<DT>(const MxParams& p, int mode, const MxPlan& plan, hipStream_t s) {
-  if (mode == kMxUp) return go<kMxUp, 64, 256, 1, 4>(p, s);
-  if (mode == kMxDown) return go<kMxDown, 64, 256, 1, 4>(p, s);
+  if (mode == kMxUp) return grouped<kMxUp>(p, plan, s);
+  if (mode == kMxDown) return grouped<kMxDown>(p, plan, s);
   MxParams q = p;
   q.ksplit = plan.ksplit;
   q.parts = static_cast<float*>(p.workspace);
