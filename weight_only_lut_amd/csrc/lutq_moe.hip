@@ -452,7 +452,7 @@ __global__ __launch_bounds__(1024) void moe_scan_kernel(int32_t* counts, int seg
 
 // FUSED: the offsets and what earlier segments hold come from the counts
 // here (32 segments of 256 experts: 32 KB per workgroup, and a launch less);
-// the first workgroup writes offsets and row tiles.
+// one workgroup more writes offsets and row tiles meanwhile.
 template <bool FUSED>
 __global__ __launch_bounds__(kSegWaves * 64) void moe_place_kernel(const int32_t* ids, int pairs, int E,
                                                                     const int32_t* counts, int segments,
@@ -464,21 +464,19 @@ __global__ __launch_bounds__(kSegWaves * 64) void moe_place_kernel(const int32_t
   int* cnt = run + kSegWaves * E;    // FUSED: [E] offsets
   int* before = cnt + E;             // FUSED: [E]
   int* tmp = before + E;
-  const int b = blockIdx.x * kPlanSegment, n = pairs - b < kPlanSegment ? pairs - b : kPlanSegment;
-  const auto id_of = [&](int i) { return ids[i]; };
-  count_pairs<kSegWaves>(run, E, b, n, id_of);
-  int live;
+  const int seg = blockIdx.x;
+  int live = 0;
   if constexpr (FUSED) {
     for (int e = threadIdx.x; e < E; e += kThreads) {
       int total = 0, earlier = 0;
-      for (int s0 = 0; s0 < segments; s0 += 8) {
-        int c[8];
+      for (int s0 = 0; s0 < segments; s0 += 16) {
+        int c[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = s0 + i < segments ? counts[(size_t)(s0 + i) * E + e] : 0;
+        for (int i = 0; i < 16; ++i) c[i] = s0 + i < segments ? counts[(size_t)(s0 + i) * E + e] : 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
           total += c[i];
-          if (s0 + i < (int)blockIdx.x) earlier += c[i];
+          if (s0 + i < seg) earlier += c[i];
         }
       }
       cnt[e] = total;
@@ -486,20 +484,24 @@ __global__ __launch_bounds__(kSegWaves * 64) void moe_place_kernel(const int32_t
     }
     __syncthreads();
     live = block_scan<kThreads>(cnt, E, tmp);
-    place_pairs<kSegWaves>(run, E, b, n, [&](int e) { return cnt[e] + before[e]; }, id_of, order);
+    if (seg == segments) {
+      write_tiles<kThreads>(cnt, live, before, tmp, E, tile_rows, plan, tiles);
+      return;
+    }
   } else {
     live = plan[E];
-    place_pairs<kSegWaves>(run, E, b, n, [&](int e) { return plan[e] + counts[(size_t)blockIdx.x * E + e]; },
-                           id_of, order);
   }
+  const int b = seg * kPlanSegment, n = pairs - b < kPlanSegment ? pairs - b : kPlanSegment;
+  const auto id_of = [&](int i) { return ids[i]; };
+  count_pairs<kSegWaves>(run, E, b, n, id_of);
+  if constexpr (FUSED)
+    place_pairs<kSegWaves>(run, E, b, n, [&](int e) { return cnt[e] + before[e]; }, id_of, order);
+  else
+    place_pairs<kSegWaves>(run, E, b, n, [&](int e) { return plan[e] + counts[(size_t)seg * E + e]; },
+                           id_of, order);
   // positions past the last pair
   for (int i = b + threadIdx.x; i < b + n; i += kThreads)
     if (i >= live) order[i] = -1;
-  if constexpr (FUSED) {
-    if (blockIdx.x) return;
-    __syncthreads();
-    write_tiles<kThreads>(cnt, live, before, tmp, E, tile_rows, plan, tiles);
-  }
 }
 
 // y[t] = the pair outputs of token t summed in the order of j, in fp32.
@@ -587,7 +589,7 @@ hipError_t launch_moe_plan(const int32_t* ids, int T, int E, int k, int32_t* pla
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (l.segments <= kPlanFusedSegments) {
-    moe_place_kernel<true><<<l.segments, kSegWaves * 64, fused, s>>>(
+    moe_place_kernel<true><<<l.segments + 1, kSegWaves * 64, fused, s>>>(
         ids, pairs, E, counts, l.segments, rows, plan, plan + l.tiles, plan + l.order);
     return hipGetLastError();
   }
