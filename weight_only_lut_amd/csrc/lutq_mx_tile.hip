@@ -277,6 +277,7 @@ hipError_t mx_tile<DT>(const MxParams& p, int mode, const MxPlan& plan, hipStrea
   else if (plan.bm == 128) e = go<kMxDense, 128, 256, 1, 4>(q, s);
   else if (plan.bm == 64 && plan.bn == 256) e = go<kMxDense, 64, 256, 1, 4>(q, s);
   else if (plan.bm == 64) e = go<kMxDense, 64, 128, 1, 4>(q, s);
+  else if (plan.bm == 48) e = go<kMxDense, 48, 128, 1, 4>(q, s);
   else e = go<kMxDense, 32, 128, 1, 4>(q, s);
   if (e != hipSuccess || q.ksplit == 1) return e;
   return launch_mx_join(q.parts, q.ksplit, q.plane,
