@@ -105,7 +105,8 @@ int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N
  * The weights enter exactly, with their row's largest scale taken out and
  * multiplied onto the fp32 sum, except that bits are lost of values in a
  * block whose scale is below its row's largest by more than 2^36 (fp16) or
- * 2^120 (bf16).
+ * 2^120 (bf16). A sum whose weights, so scaled to at most 6 (fp16: 6 * 2^13),
+ * pass the range of fp32 overflows: activations near 1e38 can.
  * path: LUTQ_MX_PATH_AUTO, or one of the two kernels (any M runs on either).
  * M == 0 or N == 0: nothing to do. K == 0: y is set to zero.
  * Errors: LUTQ_EINVAL, LUTQ_EMISMATCH, LUTQ_EALIGN, LUTQ_EUNSUPPORTED (more
@@ -122,7 +123,7 @@ int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed
 /* The same with 4-bit activations: xcodes [M][K/2] and xscales [M][K/32] as
  * lutq_mx_quantize writes them, both operands in 4 bits on the scaled matrix
  * instructions; `dtype` (fp16 or bf16) is y's.
- *   xcodes : 16-byte aligned. */
+ *   xcodes : 16-byte aligned; M * K <= LUTQ_MAX_NK. */
 int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
                       void* y, int dtype, int M, int N, int K, void* workspace,
                       size_t workspace_bytes, void* stream);

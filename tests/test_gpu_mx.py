@@ -256,6 +256,23 @@ def test_matmul_reads_and_writes_nothing_else(lutq, M, path):
     close(y, *mx.matmul(f64(x), mx.dequantize(c, s)), K, torch.bfloat16)
 
 
+@pytest.mark.parametrize("M", [3, 70, 600])
+def test_matmul_into_an_8_byte_aligned_output(lutq, M):
+    rng = np.random.default_rng(M)
+    N, K = 264, 320
+    c, s = weights(rng, N, K)
+    W = lutq.mx_pack(dev(c), dev(s))
+    x = torch.randn(M, K, device="cuda").half()
+    buf = torch.full((M * N + 8,), 7.0, dtype=torch.float16, device="cuda")
+    for src in (x, lutq.mx_quantize(x)):
+        y = lutq.mx_matmul(src, W, dtype=torch.float16, out=buf[4:4 + M * N].view(M, N))
+        assert torch.equal(y, lutq.mx_matmul(src, W, dtype=torch.float16))
+        assert bool((buf[:4] == 7).all()) and bool((buf[4 + M * N:] == 7).all())
+    with pytest.raises(lutq.LutqError) as e:
+        lutq.mx_matmul(x, W, out=buf[2:2 + M * N].view(M, N))
+    assert e.value.code == -4
+
+
 @pytest.mark.parametrize("M,N,K", [(0, 16, 64), (4, 0, 64), (4, 16, 0)])
 def test_matmul_empty(lutq, M, N, K):
     W = lutq.mx_pack(torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda"),

@@ -313,7 +313,13 @@ int run_matmul(const uint16_t* x, const lutq_matmul_item_t* items, int count, in
 
 namespace lutq {
 int record_hip_error(hipError_t e) { return hip_fail(e); }
-int device_cu_count() { return cu_count(); }
+int device_cu_count() {
+  try {
+    return cu_count();
+  } catch (...) {  // no memory for its cache
+    return 256;
+  }
+}
 }  // namespace lutq
 
 extern "C" {

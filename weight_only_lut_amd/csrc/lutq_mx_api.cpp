@@ -303,6 +303,7 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
   if (!tiles_fit((M + 63LL) / 64, N)) return LUTQ_EUNSUPPORTED;
   const hipStream_t s = (hipStream_t)stream;
   if (K == 0) return status(launch_mx_zero(y, (long long)M * N, s));
+  if ((long long)M * K > LUTQ_MAX_NK) return LUTQ_EUNSUPPORTED;
   if (!xcodes || !xscales) return LUTQ_EINVAL;
   if (!aligned(xcodes, 16)) return LUTQ_EALIGN;
   const MxPlan plan = mx_plan4(M, N, K, device_cu_count());

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
       }
     return;
   }
-  if (N % (kFloat ? 4 : 8) == 0) {
+  if (N % (kFloat ? 4 : 8) == 0 && ((uintptr_t)p.y & 15) == 0) {
     lds_ready();  // the tiles are free
     constexpr int P = kOut * (kFloat ? 4 : 2);
     constexpr int kArea = WM * WN * 16 * P;

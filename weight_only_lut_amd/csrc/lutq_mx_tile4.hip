@@ -162,7 +162,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
       }
     return;
   }
-  if (w.N % 8 == 0) {
+  if (w.N % 8 == 0 && ((uintptr_t)y & 15) == 0) {
     lds_ready();  // the tiles are free
     constexpr int P = NI * 2;
     RowStage<P> stage{ws0 + wave * (16 * P)};
