@@ -83,8 +83,9 @@ __device__ __forceinline__ uint32_t quantize8(const f32x8& v, int rule, uint32_t
   return bad ? 0u : c;
 }
 
-// UNITS units of 8 values per thread, a block's width apart so that each
+// UNITS units of 8 values per thread, a workgroup's width apart so that each
 // load and store of the workgroup is contiguous; all loads are issued first.
+// 28672 x 8192 in fp32: 5.4 TB/s read and written.
 template <int DT, int UNITS>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void* x, long long row_values,
                                                                 long long ldx, int rule,
@@ -216,11 +217,12 @@ __global__ __launch_bounds__(kThreads) void mx_pack_kernel(const uint8_t* codes,
 template <int DT>
 hipError_t quantize(const void* x, int rows, long long row_values, long long ldx, int rule,
                     uint8_t* codes, uint8_t* scales, hipStream_t s) {
-  const long long wide = 4LL * kThreads * kLaneValues, narrow = (long long)kThreads * kLaneValues;
-  // four units per thread keep enough loads in flight to stream; a call of
-  // few workgroups spreads wider instead
-  const bool few = (row_values + wide - 1) / wide * rows < 1024;
-  const long long per = few ? narrow : wide;
+  // one unit per thread until there are many times more workgroups than the
+  // device holds, then two (fp16, us at 1 / 2 / 4 units: 14.7 M values 7.7 / 8.0 /
+  // 8.3, 117 M 49.4 / 47.3 / 49.2)
+  const long long narrow = (long long)kThreads * kLaneValues;
+  const bool few = (row_values + narrow - 1) / narrow * rows < 16384;
+  const long long per = few ? narrow : 2 * narrow;
   const unsigned gx = (unsigned)((row_values + per - 1) / per);
   for (long long r0 = 0; r0 < rows; r0 += 65535) {  // grid.y
     const unsigned gy = (unsigned)(rows - r0 < 65535 ? rows - r0 : 65535);
@@ -228,7 +230,7 @@ hipError_t quantize(const void* x, int rows, long long row_values, long long ldx
     uint8_t* cr = codes + r0 * row_values / 2;
     uint8_t* sr = scales + r0 * row_values / kMxBlock;
     if (few) mx_quantize_kernel<DT, 1><<<dim3(gx, gy), kThreads, 0, s>>>(xr, row_values, ldx, rule, cr, sr);
-    else mx_quantize_kernel<DT, 4><<<dim3(gx, gy), kThreads, 0, s>>>(xr, row_values, ldx, rule, cr, sr);
+    else mx_quantize_kernel<DT, 2><<<dim3(gx, gy), kThreads, 0, s>>>(xr, row_values, ldx, rule, cr, sr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -215,11 +215,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
         const int n = n0 + piece * (kFloat ? 4 : 8);
         if (m0 + row >= rows || n >= N) return;
         if constexpr (kFloat) {
-          // nontemporal: hundreds of MB of pair outputs pass by once (24570
-          // pairs of 4096 x 1024: 258 us against 365)
           const int pair = p.order[row0 + m0 + row];
-          __builtin_nontemporal_store(__builtin_bit_cast(f32x4, v) * p.weights[pair],
-                                      reinterpret_cast<f32x4*>(y32 + (size_t)pair * N + n));
+          *reinterpret_cast<f32x4*>(y32 + (size_t)pair * N + n) = __builtin_bit_cast(f32x4, v) * p.weights[pair];
         } else {
           *reinterpret_cast<u32x4*>(y16 + (size_t)(row0 + m0 + row) * N + n) = v;
         }
