@@ -1,7 +1,8 @@
 """lutq: weight-only LUT-quantized matmul for AMD MI355X (gfx950).
 
 The compute lives in hand-written HIP kernels behind the C ABI of
-``liblutq.so`` (declared in ``include/lutq.h``); this package is a thin
+``liblutq.so`` (declared in ``include/lutq.h``,
+``lutq_mx.h`` and ``lutq_moe.h``); this package is a thin
 ctypes binding with the same names. PyTorch supplies device memory and the
 current stream only. There is no CPU fallback: if the library is missing or
 no GPU is present, the calls raise.
