@@ -16,8 +16,12 @@ constexpr int DT = LUTQ_MX_TYPE;
 typedef Mx16<DT> T;
 typedef T::frag frag;
 
+// Three workgroups of 64 x 256 share a CU where two of the larger tiles do (both
+// experts' products of 4095 tokens, 6 of 64 experts of 4096 x 1024: 665 us, with
+// two 691; fp16 keeps six registers of the prologue in memory for it).
 template <int MODE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, int mtiles, int ntiles) {
+__global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void mx_tile_kernel(
+    MxParams p, int mtiles, int ntiles) {
   constexpr bool kUp = MODE == kMxUp;
   constexpr int kThreads = WM * WN * 64;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -63,16 +67,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
   const int prow = threadIdx.x >> 4;
   const int col = lds_piece_at(threadIdx.x & 15, prow) * 8;
   // Rows in order go through a buffer resource, whose end makes rows past the
-  // last read as zeros; gathered rows take a pointer each.
+  // last read as zeros; gathered rows are found from their numbers.
   __amdgpu_buffer_rsrc_t rs;
   uint32_t at = 0, row_step = 0;
-  const uint16_t* xp[kUp ? kLoads : 1];
+  uint32_t src[kUp ? kLoads : 1];
   if constexpr (kUp) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = i * kRowStep + prow;
-      const long long src = p.order[row0 + (row < rows ? row : rows - 1)] / p.topk;
-      xp[i] = static_cast<const uint16_t*>(p.x) + src * p.ldx + col;
+      src[i] = (uint32_t)(p.order[row0 + (row < rows ? row : rows - 1)] / p.topk);
     }
   } else {
     rs = make_rsrc(static_cast<const uint16_t*>(p.x) + row0 * p.ldx,
@@ -108,7 +111,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(MxParams p, in
       if (j >= 0 && i * 4 / kLoads != j) continue;
       u32x4* dst = stage + i * kThreads + wave * kWave;
       const bool past = (c + 1) * kChunk > w.K && c * kChunk + col >= w.K;
-      if constexpr (kUp) load_to_lds(past ? static_cast<const void*>(&mx_zero16) : xp[i] + (size_t)c * kChunk, dst);
+      if constexpr (kUp)
+        load_to_lds(past ? static_cast<const void*>(&mx_zero16)
+                         : static_cast<const char*>(p.x) + c * (kChunk * 2) +
+                               ((uint64_t)src[i] * (uint32_t)(p.ldx * 2) + (uint32_t)(col * 2)),
+                    dst);
       else buffer_to_lds(rs, past ? kOutOfRange : at + i * row_step + c * (kChunk * 2), dst);
     }
   };
