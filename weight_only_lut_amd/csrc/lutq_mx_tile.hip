@@ -59,6 +59,12 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
     rows = t[2];
   }
   const MxWeights& w = p.w;
+  // The down products' outputs go to their pair's row: lane l has the pair and
+  // the weight of the tile's row l ready when they come.
+  static_assert(MODE != kMxDown || BM <= kWave, "a lane per row");
+  int pair = 0;
+  float share = 0.0f;
+  if constexpr (MODE == kMxDown) pair = p.order[row0 + (lane < rows ? lane : rows - 1)];
 
   // This thread's pieces of the activations' tile: piece i is row
   // i * kRowStep + tid / 16, and the same column for every i.
@@ -162,6 +168,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
   uint32_t s0[NI], s1[NI];
   load_x(c0, xs0, -1);
   load_w(c0, d0, s0, -1);
+  if constexpr (MODE == kMxDown) share = p.weights[pair];
   int c = c0;
   for (; c + 1 < c1; c += 2) {
     step(c, xs0, xs1, d0, s0, d1, s1);
@@ -220,11 +227,13 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
       }
       stage.drain(lane, [&](int row, int piece, u32x4 v) {
         const int n = n0 + piece * (kFloat ? 4 : 8);
-        if (m0 + row >= rows || n >= N) return;
         if constexpr (kFloat) {
-          const int pair = p.order[row0 + m0 + row];
-          *reinterpret_cast<f32x4*>(y32 + (size_t)pair * N + n) = __builtin_bit_cast(f32x4, v) * p.weights[pair];
+          const int to = __shfl(pair, m0 + row);
+          const float by = __shfl(share, m0 + row);
+          if (m0 + row >= rows || n >= N) return;
+          *reinterpret_cast<f32x4*>(y32 + (size_t)to * N + n) = __builtin_bit_cast(f32x4, v) * by;
         } else {
+          if (m0 + row >= rows || n >= N) return;
           *reinterpret_cast<u32x4*>(y16 + (size_t)(row0 + m0 + row) * N + n) = v;
         }
       });
@@ -236,11 +245,11 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
 #pragma unroll
     for (int m = 0; m < MI; ++m) {
       const int row = (wm * MI + m) * 16 + r, n = n0 + i * 16 + 4 * q;
-      if (row >= rows) continue;
       if constexpr (kFloat) {
-        const int pair = p.order[row0 + row];
-        store4(y32 + (size_t)pair * N, n, N, value(i, m) * p.weights[pair]);
-      } else {
+        const int to = __shfl(pair, row);
+        const float by = __shfl(share, row);
+        if (row < rows) store4(y32 + (size_t)to * N, n, N, value(i, m) * by);
+      } else if (row < rows) {
         store4<DT>(y16 + (size_t)(row0 + row) * N, n, N, value(i, m));
       }
     }
