@@ -190,6 +190,7 @@ template <int W, int NT, int U>
 __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
   typedef Mx16<kBf16> T;
   typedef T::frag frag;
+  static_assert(NT <= W, "a wave per output tile");
   __shared__ f32x4 red[W][NT][kWave];
   __shared__ u32x4 hs[W][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -201,6 +202,7 @@ __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
   const uint16_t* h = static_cast<const uint16_t*>(p.x) + (size_t)token * k * p.ldx;
   const __amdgpu_buffer_rsrc_t hrs = make_rsrc(h, (uint32_t)((p.plane + k * p.ldx) * 2));
   const uint32_t hoff = q < 2 ? (uint32_t)((q * p.plane + 8 * r) * 2) : kOutOfRange;
+  const int own = wave < NT && r < k ? ids[r] : -1;
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
@@ -230,6 +232,15 @@ __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u, u0 + u);
+  // Wave i < NT writes tile i's outputs; its lane (q, j) fetches what pair j's
+  // are multiplied by while the products run.
+  const bool has = (unsigned)own < (unsigned)p.experts && (int)blockIdx.x * NT + wave < w.ntile;
+  f32x4 factor = {0, 0, 0, 0};
+  float share = 0.0f;
+  if (has) {
+    factor = row_factors(w.rows + own * w.expert_rows, ((int)blockIdx.x * NT + wave) * 16 + 4 * q, T::kShift);
+    share = p.weights[(size_t)token * k + r];
+  }
   for (int b = u0; b < u1; b += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -257,24 +268,19 @@ __global__ __launch_bounds__(W * 64) void mx_down_token_kernel(MxParams p) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) red[wave][i][lane] = acc[i];
   __syncthreads();
-  // lane (q, j): the outputs n = 4q .. 4q + 3 of pair j, summed in the order of j
-  for (int s = threadIdx.x; s < NT * 4; s += W * 64) {
-    const int i = s >> 2, qq = s & 3;
-    const int t = (int)blockIdx.x * NT + i;
-    if (t >= w.ntile) continue;
-    const int n = t * 16 + 4 * qq;
-    f32x4 sum = {0, 0, 0, 0};
-    for (int j = 0; j < k; ++j) {
-      const int id = ids[j];
-      if ((unsigned)id >= (unsigned)p.experts) continue;
-      f32x4 v = red[0][i][qq * 16 + j];
+  if (threadIdx.x >= NT * kWave) return;
+  // lane (q, j): the outputs n = 4q .. 4q + 3 of pair j
+  f32x4 v = red[0][wave][lane];
 #pragma unroll
-      for (int x = 1; x < W; ++x) v += red[x][i][qq * 16 + j];
-      v *= row_factors(w.rows + id * w.expert_rows, n, T::kShift);
-      sum += v * p.weights[(size_t)token * k + j];
-    }
-    store4<DT>(static_cast<uint16_t*>(p.y) + (size_t)token * w.N, n, w.N, sum);
-  }
+  for (int x = 1; x < W; ++x) v += red[x][wave][lane];
+  v *= factor;
+  red[0][wave][lane] = has ? v * share : f32x4{0, 0, 0, 0};
+  wave_lds_order();
+  const int t = (int)blockIdx.x * NT + wave;
+  if (r || t >= w.ntile) return;
+  f32x4 sum = {0, 0, 0, 0};
+  for (int j = 0; j < k; ++j) sum += red[0][wave][q * 16 + j];
+  store4<DT>(static_cast<uint16_t*>(p.y) + (size_t)token * w.N, t * 16 + 4 * q, w.N, sum);
 }
 
 template <int MODE, int W, int NT, int RX, int U>
