@@ -337,3 +337,21 @@ def test_graph_replays_and_streams(lutq):
         y3 = lutq.mx_matmul(x3, W)
     side.synchronize()
     assert torch.equal(y3, lutq.mx_matmul(x1 * 2, W))
+
+
+@pytest.mark.parametrize("M", [1, 40, 150, 700])
+@pytest.mark.parametrize("four_bit", [False, True])
+def test_rows_of_any_width_are_whole_and_nothing_past_them_is_written(lutq, M, four_bit):
+    # the same rows of weights, one to eight cut off: the same outputs, bit for bit
+    rng = torch.Generator(device="cuda").manual_seed(M)
+    K, wide = 512, 1008
+    codes, scales = lutq.mx_quantize(torch.randn(wide, K, generator=rng, device="cuda"))
+    x = torch.randn(M, K, generator=rng, device="cuda").to(torch.bfloat16)
+    x = lutq.mx_quantize(x) if four_bit else x
+    full = lutq.mx_matmul(x, lutq.mx_pack(codes, scales))
+    for N in range(wide - 8, wide):
+        buf = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        lutq.mx_matmul(x, lutq.mx_pack(codes[:N].contiguous(), scales[:N].contiguous()),
+                       out=buf[:M * N].view(M, N))
+        assert torch.equal(buf[:M * N].view(M, N), full[:, :N]), N
+        assert torch.all(buf[M * N:] == 7.0), N

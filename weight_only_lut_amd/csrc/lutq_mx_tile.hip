@@ -18,7 +18,7 @@ typedef T::frag frag;
 
 // Three workgroups of 64 x 256 share a CU where two of the larger tiles do (both
 // experts' products of 4095 tokens, 6 of 64 experts of 4096 x 1024: 665 us, with
-// two 691; fp16 keeps six registers of the prologue in memory for it).
+// two 691).
 template <int MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void mx_tile_kernel(
     MxParams p, int mtiles, int ntiles) {
@@ -134,7 +134,14 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
       s[i] = scales[((size_t)tile[i] * w.nquad + c / 4) * (kWave * 4) + lane * 4 + c % 4];
     }
   };
-  const int base = (wm * MI * 16 + r) * 16;
+  // Where a fragment read finds its piece of a stage, in bytes. (Opaque, so
+  // that the reads of both stages share them as immediate offsets do.)
+  uint32_t from[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    from[j] = (uint32_t)(((wm * MI * 16 + r) * 16 + lds_piece(4 * q + j, r)) * 16);
+    asm volatile("" : "+v"(from[j]));
+  }
   // One chunk, in four steps of 32; a quarter of the next chunk's loads goes
   // out in each, since a wave that issues them all at once waits to do so
   // before it multiplies (the fences keep the compiler from gathering them, and
@@ -155,7 +162,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
       frag b[MI];
 #pragma unroll
       for (int m = 0; m < MI; ++m)
-        b[m] = __builtin_bit_cast(frag, cur[base + m * 256 + lds_piece(4 * q + j, r)]);
+        b[m] = *reinterpret_cast<const frag*>(reinterpret_cast<const char*>(cur + m * 256) + from[j]);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const frag a = T::decode(d[i][j], mx_scale<DT>(s[i]));
@@ -210,49 +217,36 @@ __global__ __launch_bounds__(WM * WN * 64, BM == 64 && BN == 256 ? 3 : 2) void m
       }
     return;
   }
-  if (N % (kFloat ? 4 : 8) == 0 && ((uintptr_t)p.y & 15) == 0) {
-    lds_ready();  // the tiles are free
-    constexpr int P = kOut * (kFloat ? 4 : 2);
-    constexpr int kArea = WM * WN * 16 * P;
-    __shared__ u32x4 own[kArea > BM * 16 ? kArea : 1];
-    RowStage<P> stage{(kArea > BM * 16 ? own : xs0) + wave * (16 * P)};
+  lds_ready();  // the tiles are free
+  if (n0 >= N) return;
+  constexpr int P = kOut * (kFloat ? 4 : 2);
+  constexpr int kArea = WM * WN * 16 * P;
+  __shared__ u32x4 own[kArea > BM * 16 ? kArea : 1];
+  RowStage<P> stage{(kArea > BM * 16 ? own : xs0) + wave * (16 * P)};
 #pragma unroll
-    for (int m = 0; m < MI; ++m) {
-      const int m0 = (wm * MI + m) * 16;
+  for (int m = 0; m < MI; ++m) {
+    const int m0 = (wm * MI + m) * 16;
 #pragma unroll
-      for (int i = 0; i < kOut; ++i) {
-        const f32x4 v = value(i, m);
-        if constexpr (kFloat) stage.put4(r, 4 * i + q, v);
-        else stage.put2(r, 2 * i + (q >> 1), q & 1, T::pack(v[0], v[1]), T::pack(v[2], v[3]));
-      }
-      stage.drain(lane, [&](int row, int piece, u32x4 v) {
-        const int n = n0 + piece * (kFloat ? 4 : 8);
-        if constexpr (kFloat) {
-          const int to = __shfl(pair, m0 + row);
-          const float by = __shfl(share, m0 + row);
-          if (m0 + row >= rows || n >= N) return;
-          *reinterpret_cast<f32x4*>(y32 + (size_t)to * N + n) = __builtin_bit_cast(f32x4, v) * by;
-        } else {
-          if (m0 + row >= rows || n >= N) return;
-          *reinterpret_cast<u32x4*>(y16 + (size_t)(row0 + m0 + row) * N + n) = v;
-        }
-      });
+    for (int i = 0; i < kOut; ++i) {
+      const f32x4 v = value(i, m);
+      if constexpr (kFloat) stage.put4(r, 4 * i + q, v);
+      else stage.put2(r, 2 * i + (q >> 1), q & 1, T::pack(v[0], v[1]), T::pack(v[2], v[3]));
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kOut; ++i)
-#pragma unroll
-    for (int m = 0; m < MI; ++m) {
-      const int row = (wm * MI + m) * 16 + r, n = n0 + i * 16 + 4 * q;
+    stage.drain(lane, [&](int row, int piece, u32x4 v) {
+      // (the experts' widths are whole blocks of 32, their outputs aligned)
+      const int n = n0 + piece * (kFloat ? 4 : 8);
       if constexpr (kFloat) {
-        const int to = __shfl(pair, row);
-        const float by = __shfl(share, row);
-        if (row < rows) store4(y32 + (size_t)to * N, n, N, value(i, m) * by);
-      } else if (row < rows) {
-        store4<DT>(y16 + (size_t)(row0 + row) * N, n, N, value(i, m));
+        const int to = __shfl(pair, m0 + row);
+        const float by = __shfl(share, m0 + row);
+        if (m0 + row < rows && n < N)
+          *reinterpret_cast<f32x4*>(y32 + (size_t)to * N + n) = __builtin_bit_cast(f32x4, v) * by;
+      } else if constexpr (kUp) {
+        if (m0 + row < rows && n < N) *reinterpret_cast<u32x4*>(y16 + (size_t)(row0 + m0 + row) * N + n) = v;
+      } else {
+        if (m0 + row < rows) store8(y16 + (size_t)(row0 + m0 + row) * N, n, N, v);
       }
-    }
+    });
+  }
 }
 
 template <int MODE, int BM, int BN, int WM, int WN>

@@ -162,34 +162,22 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile4_kernel(MxParams p, i
       }
     return;
   }
-  if (w.N % 8 == 0 && ((uintptr_t)y & 15) == 0) {
-    lds_ready();  // the tiles are free
-    constexpr int P = NI * 2;
-    RowStage<P> stage{ws0 + wave * (16 * P)};
-    static_assert(kWaves * 16 * P <= BN * 8, "the waves' areas fit a stage of the weights");
+  lds_ready();  // the tiles are free
+  constexpr int P = NI * 2;
+  RowStage<P> stage{ws0 + wave * (16 * P)};
+  static_assert(kWaves * 16 * P <= BN * 8, "the waves' areas fit a stage of the weights");
 #pragma unroll
-    for (int m = 0; m < MI; ++m) {
+  for (int m = 0; m < MI; ++m) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const f32x4 v = acc[i][m] * f[i];
-        stage.put2(r, 2 * i + (q >> 1), q & 1, Mx16<DT>::pack(v[0], v[1]), Mx16<DT>::pack(v[2], v[3]));
-      }
-      const int m0 = (wm * MI + m) * 16;
-      stage.drain(lane, [&](int row, int piece, u32x4 v) {
-        const int n = n0 + piece * 8;
-        if (m0 + row < rows && n < w.N)
-          *reinterpret_cast<u32x4*>(y + (size_t)(row0 + m0 + row) * w.N + n) = v;
-      });
+    for (int i = 0; i < NI; ++i) {
+      const f32x4 v = acc[i][m] * f[i];
+      stage.put2(r, 2 * i + (q >> 1), q & 1, Mx16<DT>::pack(v[0], v[1]), Mx16<DT>::pack(v[2], v[3]));
     }
-    return;
+    const int m0 = (wm * MI + m) * 16;
+    stage.drain(lane, [&](int row, int piece, u32x4 v) {
+      if (m0 + row < rows) store8(y + (size_t)(row0 + m0 + row) * w.N, n0 + piece * 8, w.N, v);
+    });
   }
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int m = 0; m < MI; ++m) {
-      const int row = (wm * MI + m) * 16 + r;
-      if (row < rows) store4<DT>(y + (size_t)(row0 + row) * w.N, n0 + i * 16 + 4 * q, w.N, acc[i][m] * f[i]);
-    }
 }
 
 // The activations' scale bytes [M][K/32] in the order of the packed weights'
