@@ -159,7 +159,7 @@ MxPlan mx_plan(int M, int N, int K, int path, int cus) {
   // rate reached by a product that fills the device (bf16, PFLOP/s: 1.49, 1.47,
   // 1.41, 1.2, 1.0, 0.8).
   static const TileShape shapes[] = {
-      {128, 512, 1, 1.0}, {128, 256, 2, 0.98}, {64, 256, 2, 0.94},
+      {128, 512, 1, 1.0}, {128, 256, 2, 0.98}, {64, 256, 3, 0.94},
       {64, 128, 2, 0.8},  {48, 128, 2, 0.7},   {32, 128, 2, 0.55}};
   plan_tiles(&p, shapes, 6, M, N, nchunk, 2.9e6, cus);
   if (p.ksplit > 1) p.workspace = (size_t)p.ksplit * mx_plane(M, N) * sizeof(float);
