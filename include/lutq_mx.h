@@ -122,7 +122,9 @@ int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed
 
 /* The same with 4-bit activations: xcodes [M][K/2] and xscales [M][K/32] as
  * lutq_mx_quantize writes them, both operands in 4 bits on the scaled matrix
- * instructions; `dtype` (fp16 or bf16) is y's.
+ * instructions (up to 16 or 32 rows the activations are decoded to bf16, which
+ * holds all their values, beside the streamed weights); `dtype` (fp16 or bf16)
+ * is y's.
  *   xcodes : 16-byte aligned; M * K <= LUTQ_MAX_NK. */
 int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_mx_packed_t* packed,
                       void* y, int dtype, int M, int N, int K, void* workspace,
@@ -132,8 +134,8 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
  * aligned, free for other use once the call's work is done; may be NULL where
  * this is 0; LUTQ_ESIZE if it is smaller): the results of a K split for a
  * lutq_mx_matmul of this path (four_bit 0), the activations' scales in tile
- * order for lutq_mx_matmul_mx (four_bit 1). Made for the current device. 0 for
- * invalid sizes. */
+ * order and the results of a K split for lutq_mx_matmul_mx (four_bit 1). Made
+ * for the current device. 0 for invalid sizes. */
 size_t lutq_mx_workspace_bytes(int M, int N, int K, int four_bit, int path);
 
 #ifdef __cplusplus

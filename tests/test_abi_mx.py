@@ -87,10 +87,12 @@ def test_matmul_refuses(lib):
         return lib.lutq_mx_matmul(P, 2, 4096, ctypes.addressof(d), P, 96, 48, 4096, 0, ws, n, None)
     assert ms(None, 0) == EINVAL and ms(P, split - 1) == ESIZE and ms(P + 8, split) == EALIGN
 
-    need = lib.lutq_mx_workspace_bytes(2, 48, 64, 1, 0)
-    assert need > 0 and lib.lutq_mx_workspace_bytes(0, 48, 64, 1, 0) == 0 == lib.lutq_mx_workspace_bytes(2, 48, 63, 1, 0)
+    # few 4-bit rows are decoded beside the weights, more need their scales in tile order
+    need = lib.lutq_mx_workspace_bytes(40, 48, 64, 1, 0)
+    assert lib.lutq_mx_workspace_bytes(2, 48, 64, 1, 0) == 0 == lib.lutq_mx_workspace_bytes(40, 48, 63, 1, 0)
+    assert need > 0 and lib.lutq_mx_workspace_bytes(0, 48, 64, 1, 0) == 0
 
-    def m4(xc=P, xs=P, y=P, dtype=2, M=2, N=48, K=64, ws=P, n=need, **over):
+    def m4(xc=P, xs=P, y=P, dtype=2, M=40, N=48, K=64, ws=P, n=need, **over):
         d = _desc(**over)
         return lib.lutq_mx_matmul_mx(xc, xs, ctypes.addressof(d), y, dtype, M, N, K, ws, n, None)
     assert m4(M=0) == OK

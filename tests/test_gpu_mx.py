@@ -355,3 +355,21 @@ def test_rows_of_any_width_are_whole_and_nothing_past_them_is_written(lutq, M, f
                        out=buf[:M * N].view(M, N))
         assert torch.equal(buf[:M * N].view(M, N), full[:, :N]), N
         assert torch.all(buf[M * N:] == 7.0), N
+
+
+@pytest.mark.parametrize("M", [1, 6, 13, 29, 70])
+def test_4_bit_rows_with_scales_far_apart_and_a_nan(lutq, M):
+    # every code under scales from 2^-127 to 2^63, one row with a NaN block
+    rng = np.random.default_rng(M)
+    N, K = 50, 416
+    c, s = weights(rng, N, K)
+    xc = rng.integers(0, 256, (M, K // 2)).astype(np.uint8)
+    xs = np.array([0, 3, 90, 127, 190], np.uint8)[rng.integers(0, 5, (M, K // 32))]
+    if M > 1:
+        xs[M // 2, 5] = 255
+    y = lutq.mx_matmul((dev(xc), dev(xs)), lutq.mx_pack(dev(c), dev(s)))
+    ref, B = mx.matmul(mx.dequantize(xc, xs), mx.dequantize(c, s))
+    if M > 1:
+        assert torch.all(torch.isnan(y[M // 2]))
+    rows = [m for m in range(M) if M == 1 or m != M // 2]
+    close(y[rows], ref[rows], B[rows], K, torch.bfloat16)

@@ -54,7 +54,8 @@ enum MxMode {
   kMxDown = 2,      // experts' down rows: h[p] -> fp32 pair output order[p], times its weight
   // streamed
   kMxUpPair = 3,    // as kMxUp for pair p itself (no order), one pair per workgroup
-  kMxDownToken = 4  // all pairs of a token: h[t * k + j] -> y[t]
+  kMxDownToken = 4, // all pairs of a token: h[t * k + j] -> y[t]
+  kMxDense4 = 5     // as kMxDense for rows in 4 bits, streamed
 };
 
 struct MxParams {

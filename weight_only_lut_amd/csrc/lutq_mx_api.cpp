@@ -94,6 +94,11 @@ bool tiles_fit(long long row_tiles, long long N) { return row_tiles * ((N + 63) 
 // tile each and reread the activations: tiles with a K split win from 17 rows
 // (4096 x 14336: 16 rows 12.8 / 12.9, 32 rows 19.1 / 14.2, 64 rows 30.7 / 19.1).
 constexpr int kStreamRows = 64, kStreamRowsNarrow = 16;
+// The same for 4-bit activations, where tiles need a launch for the scales first
+// (16 rows: 14336 x 4096 10.6 / 14.1, 4096 x 14336 14.6 / 14.6, 28672 x 8192 29.5 /
+// 30.1; 32 rows 13.0 / 15.2, 18.5 / 16.2, 37.8 / 31.7, but 4096 x 4096 7.7 / 12.1).
+constexpr int kStreamRows4 = 16, kStreamRows4Small = 32;
+constexpr long long kSmall4 = 1 << 25;  // values of a small matrix
 // Chunks of K a workgroup of a split keeps at least.
 constexpr int kSplitChunks = 4;
 
@@ -168,6 +173,11 @@ MxPlan mx_plan(int M, int N, int K, int path, int cus) {
 
 MxPlan mx_plan4(int M, int N, int K, int cus) {
   MxPlan p = {};
+  p.ksplit = 1;
+  if (M <= ((long long)N * K <= kSmall4 ? kStreamRows4Small : kStreamRows4)) {
+    p.path = LUTQ_MX_PATH_STREAM;
+    return p;
+  }
   p.path = LUTQ_MX_PATH_TILE;
   // 4.1, 3.1 and 1.9 PFLOP/s; the kernel steps by four chunks
   static const TileShape shapes[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.75}, {64, 128, 2, 0.45}};
@@ -317,7 +327,9 @@ int lutq_mx_matmul_mx(const uint8_t* xcodes, const uint8_t* xscales, const lutq_
   p.w = weights_of(packed);
   p.y = y;
   p.M = M;
-  return status(launch_mx_tile4(p, dtype, plan, s));
+  return status(plan.path == LUTQ_MX_PATH_STREAM
+                    ? launch_mx_stream(p, dtype, kMxDense4, device_cu_count(), s)
+                    : launch_mx_tile4(p, dtype, plan, s));
 }
 
 size_t lutq_moe_plan_ints(int T, int E, int k) {

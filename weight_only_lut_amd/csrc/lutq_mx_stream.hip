@@ -44,12 +44,16 @@ __device__ __forceinline__ void store_h(uint16_t* row, size_t plane, const f32x4
 // MODE (see MxMode): dense or up-pair. For up-pair half of the NT tiles are
 // gate rows and half the up rows that meet them. W waves; RX loads of 4 rows
 // cover the rows (16 * MT of them at most); U chunks are in flight per wave.
+// With activations in 4 bits (kMxDense4) a lane's 8 values are one word and
+// their block's scale byte, decoded on the way into LDS, to bf16 whatever y is:
+// it holds every level times every scale.
 template <int MODE, int W, int NT, int RX, int U>
 __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
-  constexpr bool kUp = MODE == kMxUpPair;
+  constexpr bool kUp = MODE == kMxUpPair, kFour = MODE == kMxDense4;
   constexpr int MT = (RX + 3) / 4;
-  typedef Mx16<DT> T;
-  typedef T::frag frag;
+  constexpr int OT = kFour ? kBf16 : DT;
+  typedef Mx16<OT> T;
+  typedef typename T::frag frag;
   // the waves' activations, then their sums
   __shared__ union {
     u32x4 x[W][MT * 256];
@@ -58,7 +62,7 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   int expert = 0, row0 = 0, rows = 0;
-  if constexpr (MODE == kMxDense) {
+  if constexpr (!kUp) {
     row0 = blockIdx.y * 16 * MT;
     rows = p.M - row0 < 16 * MT ? p.M - row0 : 16 * MT;
   } else {
@@ -72,13 +76,18 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   // Load i of a chunk is rows 4i + q, 16 bytes per lane, behind a buffer
   // resource. Rows past the last read the last: their columns are not stored.
   const __amdgpu_buffer_rsrc_t xrs =
-      make_rsrc(static_cast<const uint16_t*>(p.x) + (long long)(kUp ? row0 / p.topk : row0) * p.ldx,
-                (uint32_t)(((rows - 1) * p.ldx + w.K) * 2));
-  uint32_t xoff[RX];
+      kFour ? make_rsrc(static_cast<const uint8_t*>(p.x) + (long long)row0 * p.ldx, (uint32_t)(rows * p.ldx))
+            : make_rsrc(static_cast<const uint16_t*>(p.x) + (long long)(kUp ? row0 / p.topk : row0) * p.ldx,
+                        (uint32_t)(((rows - 1) * p.ldx + w.K) * 2));
+  __amdgpu_buffer_rsrc_t vrs;
+  if constexpr (kFour)
+    vrs = make_rsrc(p.xscales + (long long)row0 * (w.K / kMxBlock), (uint32_t)(rows * (w.K / kMxBlock)));
+  uint32_t xoff[RX], voff[kFour ? RX : 1];
 #pragma unroll
   for (int i = 0; i < RX; ++i) {
     const int m = 4 * i + q, in = m < rows ? m : rows - 1;
-    xoff[i] = (uint32_t)((in * p.ldx + 8 * r) * 2);
+    xoff[i] = kFour ? (uint32_t)(in * p.ldx + 4 * r) : (uint32_t)((in * p.ldx + 8 * r) * 2);
+    if constexpr (kFour) voff[i] = (uint32_t)(in * (w.K / kMxBlock) + r / 4);
   }
   TileBuffers tile[NT];
   const int half = w.ntile / 2;  // up modes: F / 16
@@ -104,8 +113,8 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
   // U chunks in flight: each slot is refilled as soon as it is used. Loads
   // past the wave's last chunk are out of range, so they touch no memory and
   // every path has the same loads outstanding.
-  u32x4 cd[U][NT], xf[U][RX];
-  uint32_t sc[U][NT];
+  u32x4 cd[U][NT], xf[kFour ? 1 : U][RX];
+  uint32_t sc[U][NT], xc[kFour ? U : 1][RX], xv[kFour ? U : 1][RX];
   auto load = [&](int u, int c) {
     const bool in = c < c1;
     const uint32_t cc = in ? (uint32_t)c : kNoChunk;
@@ -116,8 +125,16 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
     }
     const bool valid = in && c * kChunk + 8 * r < w.K;
 #pragma unroll
-    for (int i = 0; i < RX; ++i)
-      xf[u][i] = buffer16(xrs, valid ? xoff[i] + (uint32_t)c * (kChunk * 2) : kOutOfRange);
+    for (int i = 0; i < RX; ++i) {
+      if constexpr (kFour) {
+        xc[u][i] = __builtin_amdgcn_raw_buffer_load_b32(
+            xrs, valid ? xoff[i] + (uint32_t)c * (kChunk / 2) : kOutOfRange, 0, 0);
+        xv[u][i] = __builtin_amdgcn_raw_buffer_load_b8(
+            vrs, valid ? voff[i] + (uint32_t)c * (kChunk / kMxBlock) : kOutOfRange, 0, 0);
+      } else {
+        xf[u][i] = buffer16(xrs, valid ? xoff[i] + (uint32_t)c * (kChunk * 2) : kOutOfRange);
+      }
+    }
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u, c0 + u);
@@ -125,11 +142,16 @@ __global__ __launch_bounds__(W * 64) void mx_stream_kernel(MxParams p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int i = 0; i < RX; ++i) lds.x[wave][(4 * i + q) * 16 + lds_piece(r, 4 * i + q)] = xf[u][i];
+      for (int i = 0; i < RX; ++i) {
+        u32x4 v;
+        if constexpr (kFour) v = __builtin_bit_cast(u32x4, T::decode(xc[u][i], mx_scale<OT>(xv[u][i])));
+        else v = xf[u][i];
+        lds.x[wave][(4 * i + q) * 16 + lds_piece(r, 4 * i + q)] = v;
+      }
       wave_lds_order();
       float s[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) s[i] = mx_scale<DT>(sc[u][i]);
+      for (int i = 0; i < NT; ++i) s[i] = mx_scale<OT>(sc[u][i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         frag b[MT];
@@ -290,11 +312,12 @@ hipError_t go(const MxParams& p, hipStream_t s) {
   const int tiles = kUp ? p.w.ntile / 2 : p.w.ntile, per = kUp ? NT / 2 : NT;
   const unsigned gx = (unsigned)((tiles + per - 1) / per);
   MxParams q = p;
-  if constexpr (MODE == kMxDense) {
+  if constexpr (!kUp) {
     const int step = 65535 * kRows;  // grid.y
     for (int m0 = 0; m0 < p.M; m0 += step) {
       q.M = p.M - m0 < step ? p.M - m0 : step;
-      q.x = static_cast<const uint16_t*>(p.x) + (size_t)m0 * p.ldx;
+      q.x = static_cast<const uint8_t*>(p.x) + (size_t)m0 * p.ldx * (MODE == kMxDense4 ? 1 : 2);
+      if constexpr (MODE == kMxDense4) q.xscales = p.xscales + (size_t)m0 * (p.w.K / kMxBlock);
       q.y = static_cast<uint16_t*>(p.y) + (size_t)m0 * p.w.N;
       mx_stream_kernel<MODE, W, NT, RX, U>
           <<<dim3(gx, (unsigned)((q.M + kRows - 1) / kRows)), W * 64, 0, s>>>(q);
@@ -315,24 +338,27 @@ hipError_t go(const MxParams& p, hipStream_t s) {
 // there two tiles and four waves on a wide matrix (14336 x 4096: 8.4, one tile
 // and eight waves 8.7 to 10.1), one tile and eight waves on a narrow one
 // (4096 x 14336: 8.3 against 10.5 and more).
-template <int RX, int U4, int U1>
+template <int MODE, int RX, int U4, int U1>
 hipError_t by_width(const MxParams& p, int cus, hipStream_t s) {
   const int t = p.w.ntile;
-  if (5 * t >= 16 * cus) return go<kMxDense, 8, 4, RX, U4>(p, s);
-  if (5 * t >= 8 * cus) return go<kMxDense, 8, 2, RX, U4>(p, s);
-  return go<kMxDense, 8, 1, RX, U1>(p, s);
+  if (5 * t >= 16 * cus) return go<MODE, 8, 4, RX, U4>(p, s);
+  if (5 * t >= 8 * cus) return go<MODE, 8, 2, RX, U4>(p, s);
+  return go<MODE, 8, 1, RX, U1>(p, s);
 }
+template <int MODE>
 hipError_t dense(const MxParams& p, int cus, hipStream_t s) {
   if (p.M <= 4) {
-    if (p.w.ntile >= 2 * cus) return go<kMxDense, 4, 2, 1, 4>(p, s);
+    if (p.w.ntile >= 2 * cus) return go<MODE, 4, 2, 1, 4>(p, s);
     // a short K leaves a wave few chunks: 1024 x 1024 2.8 with two in flight, 3.5 with four
-    return p.w.nchunk >= 64 ? go<kMxDense, 8, 1, 1, 4>(p, s) : go<kMxDense, 8, 1, 1, 2>(p, s);
+    return p.w.nchunk >= 64 ? go<MODE, 8, 1, 1, 4>(p, s) : go<MODE, 8, 1, 1, 2>(p, s);
   }
-  if (p.M <= 8) return by_width<2, 2, 2>(p, cus, s);
-  if (p.M <= 16) return by_width<4, 2, 2>(p, cus, s);
-  if (p.M <= 32) return by_width<8, 2, 2>(p, cus, s);
-  if (p.M <= 48) return by_width<12, 1, 1>(p, cus, s);
-  return by_width<16, 1, 1>(p, cus, s);
+  if (p.M <= 8) return by_width<MODE, 2, 2, 2>(p, cus, s);
+  if (p.M <= 16) return by_width<MODE, 4, 2, 2>(p, cus, s);
+  if constexpr (MODE == kMxDense) {
+    if (p.M > 48) return by_width<MODE, 16, 1, 1>(p, cus, s);
+    if (p.M > 32) return by_width<MODE, 12, 1, 1>(p, cus, s);
+  }
+  return by_width<MODE, 8, 2, 2>(p, cus, s);  // (4-bit activations: 32 rows at most)
 }
 
 }  // namespace
@@ -340,7 +366,8 @@ hipError_t dense(const MxParams& p, int cus, hipStream_t s) {
 template <>
 hipError_t mx_stream<DT>(const MxParams& p, int mode, int cus, hipStream_t s) {
   switch (mode) {
-    case kMxDense: return dense(p, cus, s);
+    case kMxDense: return dense<kMxDense>(p, cus, s);
+    case kMxDense4: return dense<kMxDense4>(p, cus, s);
     case kMxUpPair: return go<kMxUpPair, 8, 2, 1, 4>(p, s);
     default: {
       mx_down_token_kernel<8, 1, 4><<<dim3((unsigned)p.w.ntile, (unsigned)p.M), 512, 0, s>>>(p);
