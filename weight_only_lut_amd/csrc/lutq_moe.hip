@@ -203,6 +203,8 @@ __device__ void route_token(const RouteParams& p, int t, int lane, float* keys, 
 
 constexpr int kRouteWaves = 4;
 
+// Bound by VALU work, about 700 instructions per token of 256 experts in 8
+// groups: 8191 tokens 14 us, while their logits are 1.7 us of memory.
 template <int VPT>
 __global__ __launch_bounds__(kRouteWaves * 64) void moe_route_kernel(RouteParams p) {
   __shared__ float keys[kRouteWaves][VPT * kWave];
@@ -324,6 +326,8 @@ __device__ void count_pairs(int* run, int E, int b, int n, Id id_of) {
   __syncthreads();
 }
 
+// Bound by the launch and the trip to memory: a token of 64 experts 4.3 us, of
+// which an empty launch with arguments is 2.4.
 // Few pairs: a wave per token routes (unless VPT is 0), then the first wave
 // finds each pair's position by counting the pairs before it. No row tiles:
 // the products of so few pairs do not use them.
@@ -504,7 +508,8 @@ __global__ __launch_bounds__(kSegWaves * 64) void moe_place_kernel(const int32_t
     if (i >= live) order[i] = -1;
 }
 
-// y[t] = the pair outputs of token t summed in the order of j, in fp32.
+// y[t] = the pair outputs of token t summed in the order of j, in fp32. Bound by
+// their bytes, read once: 4095 x 6 rows of 4096 64 us, 6.7 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* pairs, const int32_t* ids,
                                                            uint16_t* y, int k, int D, int E) {
@@ -527,7 +532,8 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* pairs, co
   store4<DT>(y + (size_t)t * D, n, D, sum);
 }
 
-// y = the sum of `count` planes, in their order, rounded to 16 bits.
+// y = the sum of `count` planes, in their order, rounded to 16 bits. Bound by the
+// launch and one trip to memory: 16 planes of 33 x 4096 3.9 us.
 template <int DT>
 __global__ __launch_bounds__(256) void mx_join_kernel(const float* parts, int count, long long plane,
                                                        long long values, uint16_t* y) {
