@@ -113,7 +113,7 @@ int lutq_mx_pack(const uint8_t* codes, const uint8_t* scales, int experts, int N
  * than 2^31 output tiles of 64 x 64), LUTQ_EHIP. */
 enum {
   LUTQ_MX_PATH_AUTO = 0,
-  LUTQ_MX_PATH_STREAM = 1, /* weights streamed past 16-64 rows held by a workgroup */
+  LUTQ_MX_PATH_STREAM = 1, /* weights streamed past up to 64 rows held by a workgroup */
   LUTQ_MX_PATH_TILE = 2    /* tiles of 64-256 rows through on-chip memory           */
 };
 int lutq_mx_matmul(const void* x, int dtype, long long ldx, const lutq_mx_packed_t* packed, void* y,

@@ -88,17 +88,18 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 // Whether a launch over row tiles x column tiles of at least 64 fits a grid.
 bool tiles_fit(long long row_tiles, long long N) { return row_tiles * ((N + 63) / 64) <= 0x7FFFFFFF; }
 
-// Rows up to which the stream kernel is faster than tiles (us, stream / tiles;
-// 64 rows: 14336 x 4096 17.2 / 18.8, 28672 x 8192 52 / 54; 96 rows: 28.5 / 24.3,
-// 91 / 64). On a narrow matrix with a long K its workgroups hold one weight
-// tile each and reread the activations: tiles with a K split win from 17 rows
-// (4096 x 14336: 16 rows 12.8 / 12.9, 32 rows 19.1 / 14.2, 64 rows 30.7 / 19.1).
-constexpr int kStreamRows = 64, kStreamRowsNarrow = 16;
+// Rows up to which the stream kernel is the faster (us, stream / tiles): 32 rows
+// 14336 x 4096 12.6 / 13.8, 28672 x 8192 39.0 / 41.6, 8192 x 8192 14.5 / 14.2; 48
+// rows 14.9 / 15.3, 45.0 / 42.1, 18.3 / 16.4. On a small matrix a K split and its
+// join cost more than they give: 64 rows of 4096 x 4096 10.6 / 13.3, 80 18.9 / 12.7.
+// On a narrow one with a long K the stream's workgroups hold one weight tile each
+// and reread the activations: 16 rows of 4096 x 14336 13.3 / 13.0, 32 18.9 / 14.1.
+constexpr int kStreamRows = 32, kStreamRowsSmall = 64, kStreamRowsNarrow = 16;
 // The same for 4-bit activations, where tiles need a launch for the scales first
 // (16 rows: 14336 x 4096 10.6 / 14.1, 4096 x 14336 14.6 / 14.6, 28672 x 8192 29.5 /
 // 30.1; 32 rows 13.0 / 15.2, 18.5 / 16.2, 37.8 / 31.7, but 4096 x 4096 7.7 / 12.1).
 constexpr int kStreamRows4 = 16, kStreamRows4Small = 32;
-constexpr long long kSmall4 = 1 << 25;  // values of a small matrix
+constexpr long long kSmall = 1 << 25;  // values of a small matrix
 // Chunks of K a workgroup of a split keeps at least.
 constexpr int kSplitChunks = 4;
 
@@ -155,9 +156,10 @@ MxPlan mx_plan(int M, int N, int K, int path, int cus) {
   MxPlan p = {};
   const int nchunk = (K + kChunk - 1) / kChunk;
   const bool narrow = N < 25 * cus && nchunk >= 64;  // 1.6 tiles of 16 per CU
-  p.path = path != LUTQ_MX_PATH_AUTO                              ? path
-           : M <= (narrow ? kStreamRowsNarrow : kStreamRows) ? LUTQ_MX_PATH_STREAM
-                                                             : LUTQ_MX_PATH_TILE;
+  const int stream = narrow                       ? kStreamRowsNarrow
+                     : (long long)N * K <= kSmall ? kStreamRowsSmall
+                                                  : kStreamRows;
+  p.path = path != LUTQ_MX_PATH_AUTO ? path : M <= stream ? LUTQ_MX_PATH_STREAM : LUTQ_MX_PATH_TILE;
   p.ksplit = 1;
   if (p.path == LUTQ_MX_PATH_STREAM) return p;
   // Output tiles, workgroups of it resident per CU, and the share of the best
@@ -174,7 +176,7 @@ MxPlan mx_plan(int M, int N, int K, int path, int cus) {
 MxPlan mx_plan4(int M, int N, int K, int cus) {
   MxPlan p = {};
   p.ksplit = 1;
-  if (M <= ((long long)N * K <= kSmall4 ? kStreamRows4Small : kStreamRows4)) {
+  if (M <= ((long long)N * K <= kSmall ? kStreamRows4Small : kStreamRows4)) {
     p.path = LUTQ_MX_PATH_STREAM;
     return p;
   }
