@@ -105,12 +105,12 @@ constexpr int kSplitChunks = 4;
 
 }  // namespace
 
-// us of both products of 64 experts of 4096 x 1024, 6 per token, with row tiles
-// of 16 / 32 / 64 (the better of 128 and 256 columns): 3 pairs per expert
-// 57 / 61 / 82, 12 81 / 83 / 94, 24 96 / 91 / 119, 48 147 / 121 / 143,
-// 384 836 / 602 / 560.
+// us of the block of 64 experts of 4096 x 1024, 6 per token, with row tiles of
+// 16 / 32 / 64 (the better of 128 and 256 columns): 3 pairs per expert 88 / 95 /
+// 119, 12 104 / 100 / 124, 24 132 / 119 / 124, 48 194 / 156 / 149, 72 261 / 197 /
+// 206, 96 325 / 227 / 215, 384 1071 / 733 / 644.
 int moe_tile_rows(long long pairs, int experts) {
-  return pairs <= 12LL * experts ? 16 : pairs <= 96LL * experts ? 32 : 64;
+  return pairs <= 8LL * experts ? 16 : pairs <= 80LL * experts ? 32 : 64;
 }
 
 namespace {
